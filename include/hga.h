@@ -478,6 +478,199 @@ hga_status hga_gather_store(const hga_params* p, const hga_kv_store* s, int64_t 
                             const int32_t* group_cnt, void* k_dev, void* v_dev, uint32_t* gen,
                             uint32_t step, unsigned long long* bytes, hga_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Rotary positions.  Every step above takes post-RoPE q and k; these calls make
+ * them from the projections, and turn the gradients of hga_attend_backward
+ * back into gradients of the projections.
+ *
+ * Pair i of a head's first rot_dim values turns by the angle
+ * pos[axis[i]][token] * freq[i]:
+ *   (x, y) -> (x cos - y sin, y cos + x sin);
+ * the values past rot_dim are copied.  A token has one position per axis (one
+ * axis for text; time, height and width for images and video); any int32 is a
+ * position.  Pairs are (i, i + rot_dim/2), or (2i, 2i + 1) when adjacent = 1.
+ * Angles are taken in float64 and the rotation in float32, rounded once to the
+ * output's type. */
+typedef struct hga_rope_plan {
+  const double* freq;    /* device [rot_dim/2]: radians per position            */
+  const uint8_t* axis;   /* device [rot_dim/2]: the axis of each pair, < n_axes */
+  int32_t n_axes;        /* >= 1                                                */
+  int32_t head_dim;      /* values of a head, at most 256                       */
+  int32_t rot_dim;       /* even, <= head_dim                                   */
+  int32_t adjacent;      /* 0 or 1                                              */
+} hga_rope_plan;
+
+/* One tensor of the call: heads of n tokens, the head's values contiguous.
+ * Strides are in elements.  out may be in with the same strides and types (in
+ * place), else the two must not overlap. */
+typedef struct hga_rope_io {
+  const void* in;
+  void* out;
+  int64_t in_token_stride, in_head_stride;
+  int64_t out_token_stride, out_head_stride;
+  int32_t heads;
+  int32_t in_dtype, out_dtype;   /* hga_dtype; the same in q and k              */
+} hga_rope_io;
+
+/* Rotates q and (when k is not NULL) k of n tokens in one launch.  pos: device
+ * int32, the position of token t on axis a at pos[a * pos_stride + t],
+ * pos_stride >= n.  k's output strides may be those of a [n_kv_heads][t_cap]
+ * [head_dim] cache.  An axis[i] >= n_axes sets HGA_ERR_DEVICE_CHECK. */
+hga_status hga_rope(const hga_rope_plan* r, const int32_t* pos, int64_t pos_stride, int64_t n,
+                    const hga_rope_io* q, const hga_rope_io* k, hga_stream_t stream);
+
+/* Gradients: the same call with the opposite rotation (in: gradients of the
+ * rotated values, out: gradients of the values before). */
+hga_status hga_rope_backward(const hga_rope_plan* r, const int32_t* pos, int64_t pos_stride,
+                             int64_t n, const hga_rope_io* q, const hga_rope_io* k,
+                             hga_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * A cache in pages.  The pool holds n_pages pages for each of n_planes planes
+ * (layers): page i of plane l at data + l * plane_stride + i * page_bytes.  A
+ * table row is one sequence: its tokens' pages in order, -1 where it has none,
+ * and its length in tokens.  Rows may share pages; ref counts the rows of each
+ * page, 0 = free.  Everything is device memory of the caller, and every call
+ * is asynchronous and can be captured into a graph.
+ *
+ * Lists (rows, pairs) are device int32 arrays, taken as if one entry after
+ * another.  A negative row (in hga_pages_copy: both pages negative) is skipped, so
+ * that a list of fixed size can be padded.  What cannot be done sets
+ * HGA_ERR_DEVICE_CHECK, and that entry is left undone.  Calls on one pool are
+ * ordered by the caller (one stream, or events): they share its workspace. */
+typedef struct hga_page_pool {
+  void* data;            /* 16-byte aligned; NULL when only tables are kept     */
+  int64_t page_bytes;    /* a multiple of 16                                    */
+  int64_t plane_stride;  /* bytes, a multiple of 16, >= n_pages * page_bytes    */
+  int32_t n_pages;
+  int32_t n_planes;
+  int32_t page_tokens;   /* a multiple of 8                                     */
+  int32_t n_rows;
+  int32_t row_pages;     /* entries of a table row                              */
+  int32_t* table;        /* [n_rows][row_pages]                                 */
+  int32_t* len;          /* [n_rows]                                            */
+  int32_t* ref;          /* [n_pages]                                           */
+  int32_t* work;         /* hga_pages_work_ints(pool) int32                     */
+} hga_page_pool;
+
+/* int32 words of workspace the pool needs; -1 on a bad pool. */
+int64_t hga_pages_work_ints(const hga_page_pool* pool);
+
+/* Row rows[i] grows to new_len[i] tokens: the pages it lacks are the lowest
+ * free ones, in list order.  Refused: a row outside the table, a row listed
+ * before, a new_len below the length or beyond row_pages; when the pages run
+ * out, that entry and every later one that needs a page.  n <= n_rows. */
+hga_status hga_pages_reserve(const hga_page_pool* pool, const int32_t* rows,
+                             const int32_t* new_len, int32_t n, hga_stream_t stream);
+
+/* Row children[i] becomes a copy of row parents[i].  Whole pages are shared;
+ * the last page, when it ends inside, is copied (in every plane) into the
+ * lowest free one, so that both can grow.  Refused: rows outside the table, a
+ * child that is not empty (length 0) or listed before, a parent that is also a
+ * child of the call; when the pages run out, that entry and every later one
+ * that needs a page.  n <= n_rows.  A row's whole pages are never written
+ * again; a row must not shrink while it shares pages. */
+hga_status hga_pages_fork(const hga_page_pool* pool, const int32_t* parents,
+                          const int32_t* children, int32_t n, hga_stream_t stream);
+
+/* Returns the rows' pages (a page is free once no row has it) and empties the
+ * rows: entries -1, length 0.  A row listed twice is freed once.  n <= n_rows. */
+hga_status hga_pages_free(const hga_page_pool* pool, const int32_t* rows, int32_t n,
+                          hga_stream_t stream);
+
+/* Moves the used pages together: with u pages in use, those at or above u move
+ * (in every plane), in ascending order, into the free pages below u, in
+ * ascending order; table and ref follow.  Afterwards pages [0, u) are in use. */
+hga_status hga_pages_compact(const hga_page_pool* pool, hga_stream_t stream);
+
+/* Copies page src[i] to page dst[i] in every plane; tables and ref stay as they
+ * are.  Refused: pages outside the pool, a target that an earlier pair has,
+ * a target that is also a source of the call.  n <= n_pages. */
+hga_status hga_pages_copy(const hga_page_pool* pool, const int32_t* src, const int32_t* dst,
+                          int32_t n, hga_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * K/V in 4 bits, in the pages of a pool, and the attention that reads it.
+ *
+ * 16 neighbouring values of a head share a scale.  A scale is a byte b that
+ * stands for the IEEE half with bits b << 7 (5 exponent, 3 mantissa bits): the
+ * smallest one with 6 scale >= max|x|, at most 10240.  A code is 4 bits (sign,
+ * magnitude 0 .5 1 1.5 2 3 4 6), the nearest to x / scale, ties to the even
+ * code.  Values beyond +-61440 are stored as +-61440 and NaN as 0, and both set
+ * HGA_ERR_DEVICE_CHECK.  A code times its scale is exact in bf16, fp16 and fp32.
+ *
+ * A record holds 8 tokens of one KV head: K codes [8][d/2], V codes [8][d/2]
+ * (dim 2i in the low nibble of byte i), K scales [8][d/16], V scales [8][d/16]:
+ * 9 d bytes.  A page is [n_kv_heads][page_tokens / 8] records, page_bytes =
+ * n_kv_heads * page_tokens / 8 * 9 d.  plane selects the pool's plane (layer).
+ *
+ * A batch is the sequences of one call.  Sequence i is table row rows[i] and
+ * has off[i + 1] - off[i] tokens in the call's packed arrays ([n_tok] rows),
+ * its last ones: token j of n stands at position len[rows[i]] - n + j, where
+ * len is the pool's (grow the rows with hga_pages_reserve first).  off = NULL:
+ * one token each (a decode step).  rows[i] < 0 marks an inactive sequence
+ * (padding): nothing is stored for it, and its attention output is 0 with lse
+ * -inf.  Packed rows at or past off[n_seq] are neither read nor written. */
+typedef struct hga_q4_batch {
+  const int32_t* rows;   /* device [n_seq]                                      */
+  const int32_t* off;    /* device [n_seq + 1], ascending from 0, or NULL       */
+  int32_t n_seq;
+  int32_t max_q;         /* most tokens of a sequence (1 with off = NULL)       */
+} hga_q4_batch;
+
+/* Bytes of a page of page_tokens tokens; -1 on invalid arguments. */
+int64_t hga_q4_page_bytes(const hga_params* p, int32_t page_tokens);
+
+/* Stores the K and V of the batch's tokens.  k, v: dtype, value d of head h of
+ * packed token t at k[t * k_token_stride + h * k_head_stride + d]; 16-byte
+ * aligned, strides multiples of 16 bytes.  n_tok: packed rows.  A position the
+ * row has no page for, or a row named by two sequences, sets
+ * HGA_ERR_DEVICE_CHECK.  The pages written must not be shared (hga_pages_fork
+ * leaves the page being filled to one row). */
+hga_status hga_q4_append(const hga_params* p, const hga_page_pool* pool, int32_t plane,
+                         const hga_q4_batch* b, int64_t n_tok, const void* k,
+                         int64_t k_token_stride, int64_t k_head_stride, const void* v,
+                         int64_t v_token_stride, int64_t v_head_stride, hga_stream_t stream);
+
+/* Reads the batch's tokens back into k and v (layouts as hga_q4_append; v in
+ * fp16 with params.v_f16 = 1), exact.  With the strides of a [n_kv_heads][t_cap]
+ * [head_dim] cache it fills the buffers that hga_attend and
+ * hga_attend_backward read. */
+hga_status hga_q4_read(const hga_params* p, const hga_page_pool* pool, int32_t plane,
+                       const hga_q4_batch* b, int64_t n_tok, void* k, int64_t k_token_stride,
+                       int64_t k_head_stride, void* v, int64_t v_token_stride,
+                       int64_t v_head_stride, hga_stream_t stream);
+
+/* Dense causal attention of the batch's tokens: the query at position pos of a
+ * sequence attends its tokens [0, pos].  q, o: [n_tok][n_q_heads][head_dim] in
+ * dtype, lse [n_tok][n_q_heads] float32 or NULL.  max_ctx: an upper bound of
+ * the sequences' lengths (sizes the split of long contexts; results stay right
+ * beyond it).  work: device, 16-byte aligned, hga_q4_attend_work(...) bytes,
+ * not shared by calls that may overlap.  A sequence with fewer tokens than
+ * queries sets HGA_ERR_DEVICE_CHECK and gives 0 and -inf; so do missing pages,
+ * whose tokens are left out, and a sequence of more than max_q tokens or with
+ * rows past n_tok, whose outputs stay as they are.  Results do not depend on timing. */
+hga_status hga_q4_attend(const hga_params* p, const hga_page_pool* pool, int32_t plane,
+                         const hga_q4_batch* b, int64_t n_tok, const void* q, int64_t max_ctx,
+                         void* o, float* lse, void* work, int64_t work_bytes,
+                         hga_stream_t stream);
+int64_t hga_q4_attend_work(const hga_params* p, int32_t n_seq, int32_t max_q, int64_t n_tok,
+                           int64_t max_ctx);
+
+/* hga_attend with K and V in 4 bits: the sequence is table row `row` (host
+ * value), whose pages hold the context's tokens [0, q_start + n_q); q, q_start,
+ * n_q, group_idx, group_cnt, o and lse as in hga_attend, with t_cap the capacity
+ * that the index arrays were made for.  Rows of positions before pos_lo are left
+ * as they are (a decode step attends its last row only: pos_lo = q_start + n_q
+ * - 1; q_start computes every row).  work as above,
+ * hga_q4_attend_routed_work(...) bytes. */
+hga_status hga_q4_attend_routed(const hga_params* p, const hga_page_pool* pool, int32_t plane,
+                                int32_t row, const void* q, int64_t q_start, int64_t n_q,
+                                int64_t pos_lo, int64_t t_cap, const int32_t* group_idx,
+                                const int32_t* group_cnt, void* o, float* lse, void* work,
+                                int64_t work_bytes, hga_stream_t stream);
+int64_t hga_q4_attend_routed_work(const hga_params* p, int64_t n_q);
+
 /* Slots per (KV head, block) of chunk_idx (which = 0) or group_idx
  * (which = 1) for a context capacity t_cap; -1 on invalid parameters. */
 int64_t hga_index_capacity(const hga_params* p, int64_t t_cap, int32_t which);

@@ -22,6 +22,10 @@
 #include "tier.cuh"
 #include "noalloc.cuh"
 #include "convert_v.cuh"
+#include "rope.cuh"
+#include "pages.cuh"
+#include "q4.cuh"
+#include "q4_attend.cuh"
 
 namespace {
 
@@ -1047,6 +1051,453 @@ hga_status hga_gather_history_noalloc(const hga_params* p, int64_t q_start, int6
   if ((s = after_launch()) != HGA_OK) return s;
   return hga_gather_history(p, q_start, n_q, t_cap, t_hist, group_idx, group_cnt, k_host,
                             v_host, k_dev, v_dev, gen, 1u, bytes, stream);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- rotary positions
+namespace {
+
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+template <typename TI, typename TO, int VEC>
+hga_status launch_rope(const hga::RopeArgs& a, cudaStream_t st) {
+  const int64_t blocks = (a.n + a.toks - 1) / a.toks;
+  if (blocks > 0x7fffffff) return HGA_ERR_UNSUPPORTED;
+  return launch_pdl(hga::rope_kernel<TI, TO, VEC>, dim3((unsigned)blocks), dim3(hga::kRopeThreads),
+                    0, st, a);
+}
+
+template <typename TI, typename TO>
+hga_status launch_rope_vec(const hga::RopeArgs& a, bool vec, cudaStream_t st) {
+  return vec ? launch_rope<TI, TO, 8>(a, st) : launch_rope<TI, TO, 1>(a, st);
+}
+
+hga_status rope_common(const hga_rope_plan* r, const int32_t* pos, int64_t pos_stride, int64_t n,
+                       const hga_rope_io* q, const hga_rope_io* k, float sign, cudaStream_t st) {
+  if (!r || !q) return HGA_ERR_INVALID_ARG;
+  if (r->n_axes < 1 || r->head_dim < 1 || r->rot_dim < 0 || r->rot_dim % 2 ||
+      r->rot_dim > r->head_dim || (r->adjacent != 0 && r->adjacent != 1))
+    return HGA_ERR_INVALID_ARG;
+  if (n < 0 || pos_stride < n) return HGA_ERR_INVALID_ARG;
+  const hga_rope_io* ios[2] = {q, k};
+  hga::RopeArgs a{};
+  const int half = r->rot_dim / 2;
+  bool vec = half % 8 == 0 && r->head_dim % 8 == 0;
+  for (int i = 0; i < 2; ++i) {
+    const hga_rope_io* x = ios[i];
+    if (!x) continue;
+    if (x->heads < 1 || (x->in_dtype != HGA_BF16 && x->in_dtype != HGA_FP32) ||
+        (x->out_dtype != HGA_BF16 && x->out_dtype != HGA_FP32))
+      return HGA_ERR_INVALID_ARG;
+    if (x->in_dtype != q->in_dtype || x->out_dtype != q->out_dtype) return HGA_ERR_INVALID_ARG;
+    const uintptr_t ei = x->in_dtype == HGA_BF16 ? 2 : 4, eo = x->out_dtype == HGA_BF16 ? 2 : 4;
+    if (n > 0 && (!x->in || !x->out || reinterpret_cast<uintptr_t>(x->in) % ei ||
+                  reinterpret_cast<uintptr_t>(x->out) % eo))
+      return HGA_ERR_INVALID_ARG;
+    vec = vec && aligned16(x->in) && aligned16(x->out) && x->in_token_stride % 8 == 0 &&
+          x->in_head_stride % 8 == 0 && x->out_token_stride % 8 == 0 && x->out_head_stride % 8 == 0;
+    a.io[i] = {x->in, x->out, x->in_token_stride, x->in_head_stride, x->out_token_stride,
+               x->out_head_stride};
+  }
+  if (r->head_dim > hga::kRopeMaxDim) return HGA_ERR_UNSUPPORTED;
+  if (n == 0) return HGA_OK;
+  if (half > 0 && (!pos || !r->freq || !r->axis)) return HGA_ERR_INVALID_ARG;
+  a.freq = r->freq;
+  a.axis = r->axis;
+  a.pos = pos;
+  a.pos_stride = pos_stride;
+  a.n = n;
+  a.n_axes = r->n_axes;
+  a.half = half;
+  a.d = r->head_dim;
+  a.adjacent = r->adjacent;
+  a.heads0 = q->heads;
+  a.heads = q->heads + (k ? k->heads : 0);
+  a.toks = n >= 148 * 8 ? 4 : 1;
+  a.sign = sign;
+  if (q->in_dtype == HGA_BF16)
+    return q->out_dtype == HGA_BF16 ? launch_rope_vec<__nv_bfloat16, __nv_bfloat16>(a, vec, st)
+                                    : launch_rope_vec<__nv_bfloat16, float>(a, vec, st);
+  return q->out_dtype == HGA_BF16 ? launch_rope_vec<float, __nv_bfloat16>(a, vec, st)
+                                  : launch_rope_vec<float, float>(a, vec, st);
+}
+
+// ---------------------------------------------------------------- page pools
+
+hga_status check_pool(const hga_page_pool* p, bool data) {
+  if (!p) return HGA_ERR_INVALID_ARG;
+  if (p->n_pages < 1 || p->n_planes < 1 || p->n_rows < 1 || p->row_pages < 1 ||
+      p->page_tokens < 8 || p->page_tokens % 8)
+    return HGA_ERR_INVALID_ARG;
+  if (!p->table || !p->len || !p->ref) return HGA_ERR_INVALID_ARG;
+  if (p->page_bytes < 16 || p->page_bytes % 16 || p->plane_stride % 16 ||
+      p->plane_stride / p->page_bytes < p->n_pages)
+    return HGA_ERR_INVALID_ARG;
+  if ((data && !p->data) || !aligned16(p->data)) return HGA_ERR_INVALID_ARG;
+  // positions, page ranks and table entries are counted in 32 bits
+  if ((int64_t)p->row_pages * p->page_tokens > 0x7fffffff || p->n_pages > 1 << 30 ||
+      (int64_t)p->n_rows * p->row_pages > 0x7fffffff)
+    return HGA_ERR_UNSUPPORTED;
+  return HGA_OK;
+}
+
+int64_t pool_list_ints(const hga_page_pool* p) { return std::max(p->n_pages, p->n_rows); }
+
+hga_status pool_args(const hga_page_pool* p, hga::PoolArgs* a) {
+  hga_status s = check_pool(p, false);
+  if (s != HGA_OK) return s;
+  if (!p->work) return HGA_ERR_INVALID_ARG;
+  const int64_t m = pool_list_ints(p);
+  *a = hga::PoolArgs{static_cast<char*>(p->data), p->page_bytes, p->plane_stride, p->n_pages,
+                     p->data ? p->n_planes : 0, p->page_tokens, p->n_rows, p->row_pages,
+                     p->table, p->len, p->ref};
+  a->count = p->work;
+  a->wa = a->count + 8;
+  a->wb = a->wa + m;
+  a->wc = a->wb + m;
+  a->claim = a->wc + m;
+  a->need = a->claim + 2 * (int64_t)p->n_rows;
+  return HGA_OK;
+}
+
+// Blocks of a page copy whose size only the device may know.
+unsigned copy_grid(const hga::PoolArgs& a, int64_t n) {
+  const int64_t pieces = (a.page_bytes / 16 + 4 * hga::kCopyThreads - 1) / (4 * hga::kCopyThreads);
+  const int64_t total = std::max<int64_t>(1, pieces * a.n_planes * n);
+  return (unsigned)std::min<int64_t>(std::max<int64_t>(total, n), 148 * 8);
+}
+
+hga_status q4_cache(const hga_params* p, const hga_page_pool* pool, int32_t plane,
+                    hga::Q4Cache* c) {
+  hga_status s = check_params(p);
+  if (s != HGA_OK) return s;
+  if ((s = check_pool(pool, true)) != HGA_OK) return s;
+  if (plane < 0 || plane >= pool->n_planes) return HGA_ERR_INVALID_ARG;
+  const int64_t need = (int64_t)p->n_kv_heads * (pool->page_tokens / 8) *
+                       hga::q4_record_bytes(p->head_dim);
+  if (pool->page_bytes != need) return HGA_ERR_INVALID_ARG;
+  *c = hga::Q4Cache{static_cast<char*>(pool->data) + plane * pool->plane_stride, pool->page_bytes,
+                    pool->table, pool->len, pool->n_pages, pool->n_rows, pool->row_pages,
+                    pool->page_tokens / 8, pool->page_tokens, p->n_kv_heads};
+  return HGA_OK;
+}
+
+hga_status check_batch(const hga_q4_batch* b, int64_t n_tok) {
+  if (!b || b->n_seq < 0 || b->max_q < 0 || n_tok < 0) return HGA_ERR_INVALID_ARG;
+  if (!b->off && b->max_q > 1) return HGA_ERR_INVALID_ARG;
+  if (b->n_seq > 0 && !b->rows) return HGA_ERR_INVALID_ARG;
+  if (!b->off && n_tok < b->n_seq) return HGA_ERR_INVALID_ARG;
+  return HGA_OK;
+}
+
+hga_status q4_io_args(const hga_params* p, const hga_page_pool* pool, int32_t plane,
+                      const hga_q4_batch* b, int64_t n_tok, const void* k, int64_t kt, int64_t kh,
+                      const void* v, int64_t vt, int64_t vh, int ke, int ve, hga::Q4IoArgs* a) {
+  hga_status s = q4_cache(p, pool, plane, &a->c);
+  if (s != HGA_OK) return s;
+  if ((s = check_batch(b, n_tok)) != HGA_OK) return s;
+  if (n_tok == 0 || b->n_seq == 0) return HGA_OK;
+  if (!k || !v || !aligned16(k) || !aligned16(v)) return HGA_ERR_INVALID_ARG;
+  if ((kt * ke) % 16 || (kh * ke) % 16 || (vt * ve) % 16 || (vh * ve) % 16)
+    return HGA_ERR_INVALID_ARG;
+  a->b = hga::Q4BatchArgs{b->rows, b->off, b->n_seq};
+  a->k = k;
+  a->v = v;
+  a->k_tok = kt;
+  a->k_head = kh;
+  a->v_tok = vt;
+  a->v_head = vh;
+  a->n_tok = n_tok;
+  a->D = p->head_dim;
+  return HGA_OK;
+}
+
+unsigned q4_io_grid(const hga::Q4IoArgs& a) {
+  const int64_t total = a.n_tok * a.c.Hkv * (a.D / 16);
+  return (unsigned)std::min<int64_t>((total + hga::kQ4Threads - 1) / hga::kQ4Threads, 1 << 20);
+}
+
+// ---------------------------------------------------------------- 4-bit attention
+
+// How a call is cut: rows per tile, tiles of a unit, CTAs per unit and tile.
+struct Q4Plan {
+  int nt = 1, n_tiles = 1, n_split = 1;
+  int64_t parts(int64_t units) const { return n_split > 1 ? units * n_tiles * n_split : 0; }
+};
+
+constexpr int64_t kQ4TargetCtas = 148 * 4;
+
+Q4Plan q4_plan(const hga_params* p, int64_t units, int64_t rows, int64_t max_tok) {
+  Q4Plan pl;
+  pl.nt = p->dtype == HGA_BF16 && rows > 8 ? 2 : 1;
+  pl.n_tiles = (int)((rows + 8 * pl.nt - 1) / (8 * pl.nt));
+  const int64_t ctas = std::max<int64_t>(1, units * pl.n_tiles);
+  // a split of at least one step (64 tokens) for every warp
+  const int64_t most = std::max<int64_t>(1, (max_tok + 64 * hga::kQ4Warps - 1) / (64 * hga::kQ4Warps));
+  pl.n_split = (int)std::min<int64_t>(most, (kQ4TargetCtas + ctas - 1) / ctas);
+  return pl;
+}
+
+int64_t q4_work_bytes(const hga_params* p, int64_t parts, int nt) {
+  return parts * 8 * nt * ((int64_t)p->head_dim * 4 + 8);
+}
+
+template <int D, int NT, typename T, bool ROUTED>
+hga_status launch_q4_attend(hga::Q4AttendArgs& g, int64_t nz, cudaStream_t st) {
+  using L = hga::Q4Layout<D, NT, ROUTED>;
+  const size_t smem = L::smem_bytes(ROUTED ? g.a.max_list : 0);
+  hga_status s = allow_smem<hga::q4_attend_kernel<D, NT, T, ROUTED>>(smem);
+  if (s != HGA_OK) return s;
+  dim3 grid((unsigned)(g.n_tiles * g.n_split), g.a.Hkv, (unsigned)nz);
+  s = launch_pdl(hga::q4_attend_kernel<D, NT, T, ROUTED>, grid, dim3(32 * hga::kQ4Warps), smem, st,
+                 g);
+  if (s != HGA_OK || g.n_split == 1) return s;
+  return launch_pdl(hga::q4_join_kernel<D, NT, T, ROUTED>,
+                    dim3((unsigned)g.n_tiles, g.a.Hkv, (unsigned)nz), dim3(128), 0, st, g);
+}
+
+template <bool ROUTED>
+hga_status q4_dispatch(const hga_params* p, hga::Q4AttendArgs& g, const Q4Plan& pl, int64_t nz,
+                       cudaStream_t st) {
+  const bool d128 = p->head_dim == 128;
+  if (p->dtype == HGA_FP32)
+    return d128 ? launch_q4_attend<128, 1, float, ROUTED>(g, nz, st)
+                : launch_q4_attend<64, 1, float, ROUTED>(g, nz, st);
+  if (pl.nt == 1)
+    return d128 ? launch_q4_attend<128, 1, __nv_bfloat16, ROUTED>(g, nz, st)
+                : launch_q4_attend<64, 1, __nv_bfloat16, ROUTED>(g, nz, st);
+  return d128 ? launch_q4_attend<128, 2, __nv_bfloat16, ROUTED>(g, nz, st)
+              : launch_q4_attend<64, 2, __nv_bfloat16, ROUTED>(g, nz, st);
+}
+
+void q4_common_args(const hga_params* p, const void* q, void* o, float* lse, const Q4Plan& pl,
+                    int64_t units, void* work, hga::Q4AttendArgs* g) {
+  g->a.q = q;
+  g->a.o = o;
+  g->a.lse = lse;
+  g->a.Hq = p->n_q_heads;
+  g->a.Hkv = p->n_kv_heads;
+  g->a.G = p->n_q_heads / p->n_kv_heads;
+  g->a.scale_log2 = (float)(1.4426950408889634 / sqrt((double)p->head_dim));
+  g->n_tiles = pl.n_tiles;
+  g->n_split = pl.n_split;
+  g->part_o = static_cast<float*>(work);
+  g->part_ml = reinterpret_cast<float2*>(static_cast<char*>(work) +
+                                         pl.parts(units) * 8 * pl.nt * p->head_dim * 4);
+}
+
+}  // namespace
+
+extern "C" {
+
+hga_status hga_rope(const hga_rope_plan* r, const int32_t* pos, int64_t pos_stride, int64_t n,
+                    const hga_rope_io* q, const hga_rope_io* k, hga_stream_t stream) {
+  return rope_common(r, pos, pos_stride, n, q, k, 1.0f, reinterpret_cast<cudaStream_t>(stream));
+}
+
+hga_status hga_rope_backward(const hga_rope_plan* r, const int32_t* pos, int64_t pos_stride,
+                             int64_t n, const hga_rope_io* q, const hga_rope_io* k,
+                             hga_stream_t stream) {
+  return rope_common(r, pos, pos_stride, n, q, k, -1.0f, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int64_t hga_pages_work_ints(const hga_page_pool* pool) {
+  if (!pool || pool->n_pages < 1 || pool->n_rows < 1) return -1;
+  return 8 + 3 * pool_list_ints(pool) + 3 * (int64_t)pool->n_rows;
+}
+
+hga_status hga_pages_reserve(const hga_page_pool* pool, const int32_t* rows,
+                             const int32_t* new_len, int32_t n, hga_stream_t stream) {
+  hga::PoolArgs a;
+  hga_status s = pool_args(pool, &a);
+  if (s != HGA_OK) return s;
+  if (n < 0 || n > pool->n_rows) return HGA_ERR_INVALID_ARG;
+  if (n == 0) return HGA_OK;
+  if (!rows || !new_len) return HGA_ERR_INVALID_ARG;
+  return launch_pdl(hga::pages_reserve_kernel, dim3(1), dim3(hga::kPlanThreads), 0,
+                    reinterpret_cast<cudaStream_t>(stream), a, rows, new_len, n);
+}
+
+hga_status hga_pages_fork(const hga_page_pool* pool, const int32_t* parents,
+                          const int32_t* children, int32_t n, hga_stream_t stream) {
+  hga::PoolArgs a;
+  hga_status s = pool_args(pool, &a);
+  if (s != HGA_OK) return s;
+  if (n < 0 || n > pool->n_rows) return HGA_ERR_INVALID_ARG;
+  if (n == 0) return HGA_OK;
+  if (!parents || !children) return HGA_ERR_INVALID_ARG;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if ((s = launch_pdl(hga::pages_fork_plan_kernel, dim3(1), dim3(hga::kPlanThreads), 0, st, a,
+                      parents, children, n)) != HGA_OK)
+    return s;
+  return launch_pdl(hga::pages_fork_kernel, dim3(copy_grid(a, n)), dim3(hga::kCopyThreads), 0, st,
+                    a, parents, children, n);
+}
+
+hga_status hga_pages_free(const hga_page_pool* pool, const int32_t* rows, int32_t n,
+                          hga_stream_t stream) {
+  hga::PoolArgs a;
+  hga_status s = pool_args(pool, &a);
+  if (s != HGA_OK) return s;
+  if (n < 0 || n > pool->n_rows) return HGA_ERR_INVALID_ARG;
+  if (n == 0) return HGA_OK;
+  if (!rows) return HGA_ERR_INVALID_ARG;
+  return launch_pdl(hga::pages_free_kernel, dim3(n), dim3(hga::kCopyThreads), 0,
+                    reinterpret_cast<cudaStream_t>(stream), a, rows);
+}
+
+hga_status hga_pages_compact(const hga_page_pool* pool, hga_stream_t stream) {
+  hga::PoolArgs a;
+  hga_status s = pool_args(pool, &a);
+  if (s != HGA_OK) return s;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if ((s = launch_pdl(hga::pages_compact_plan_kernel, dim3(1), dim3(hga::kPlanThreads), 0, st,
+                      a)) != HGA_OK)
+    return s;
+  if ((s = launch_pdl(hga::pages_compact_kernel, dim3(copy_grid(a, pool->n_pages)),
+                      dim3(hga::kCopyThreads), 0, st, a)) != HGA_OK)
+    return s;
+  return launch_pdl(hga::pages_compact_ref_kernel,
+                    dim3((unsigned)std::min((pool->n_pages + 255) / 256, 148)),
+                    dim3(hga::kCopyThreads), 0, st, a);
+}
+
+hga_status hga_pages_copy(const hga_page_pool* pool, const int32_t* src, const int32_t* dst,
+                          int32_t n, hga_stream_t stream) {
+  hga::PoolArgs a;
+  hga_status s = pool_args(pool, &a);
+  if (s != HGA_OK) return s;
+  if (!pool->data || n < 0 || n > pool->n_pages) return HGA_ERR_INVALID_ARG;
+  if (n == 0) return HGA_OK;
+  if (!src || !dst) return HGA_ERR_INVALID_ARG;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if ((s = launch_pdl(hga::pages_copy_plan_kernel, dim3(1), dim3(hga::kPlanThreads), 0, st, a, src,
+                      dst, n)) != HGA_OK)
+    return s;
+  return launch_pdl(hga::pages_copy_kernel, dim3(copy_grid(a, n)), dim3(hga::kCopyThreads), 0, st,
+                    a, n);
+}
+
+int64_t hga_q4_page_bytes(const hga_params* p, int32_t page_tokens) {
+  if (check_params(p) != HGA_OK || page_tokens < 8 || page_tokens % 8) return -1;
+  return (int64_t)p->n_kv_heads * (page_tokens / 8) * hga::q4_record_bytes(p->head_dim);
+}
+
+hga_status hga_q4_append(const hga_params* p, const hga_page_pool* pool, int32_t plane,
+                         const hga_q4_batch* b, int64_t n_tok, const void* k,
+                         int64_t k_token_stride, int64_t k_head_stride, const void* v,
+                         int64_t v_token_stride, int64_t v_head_stride, hga_stream_t stream) {
+  hga::Q4IoArgs a{};
+  const int e = p && p->dtype == HGA_BF16 ? 2 : 4;
+  hga_status s = q4_io_args(p, pool, plane, b, n_tok, k, k_token_stride, k_head_stride, v,
+                            v_token_stride, v_head_stride, e, e, &a);
+  if (s != HGA_OK || n_tok == 0 || b->n_seq == 0) return s;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return p->dtype == HGA_BF16
+             ? launch_pdl(hga::q4_append_kernel<__nv_bfloat16>, dim3(q4_io_grid(a)),
+                          dim3(hga::kQ4Threads), 0, st, a)
+             : launch_pdl(hga::q4_append_kernel<float>, dim3(q4_io_grid(a)),
+                          dim3(hga::kQ4Threads), 0, st, a);
+}
+
+hga_status hga_q4_read(const hga_params* p, const hga_page_pool* pool, int32_t plane,
+                       const hga_q4_batch* b, int64_t n_tok, void* k, int64_t k_token_stride,
+                       int64_t k_head_stride, void* v, int64_t v_token_stride,
+                       int64_t v_head_stride, hga_stream_t stream) {
+  hga::Q4IoArgs a{};
+  const int e = p && p->dtype == HGA_BF16 ? 2 : 4;
+  hga_status s = q4_io_args(p, pool, plane, b, n_tok, k, k_token_stride, k_head_stride, v,
+                            v_token_stride, v_head_stride, e, e, &a);
+  if (s != HGA_OK || n_tok == 0 || b->n_seq == 0) return s;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const dim3 grid(q4_io_grid(a)), block(hga::kQ4Threads);
+  if (p->dtype == HGA_FP32)
+    return launch_pdl(hga::q4_read_kernel<float, float>, grid, block, 0, st, a);
+  return p->v_f16 ? launch_pdl(hga::q4_read_kernel<__nv_bfloat16, __half>, grid, block, 0, st, a)
+                  : launch_pdl(hga::q4_read_kernel<__nv_bfloat16, __nv_bfloat16>, grid, block, 0,
+                               st, a);
+}
+
+int64_t hga_q4_attend_work(const hga_params* p, int32_t n_seq, int32_t max_q, int64_t n_tok,
+                           int64_t max_ctx) {
+  if (check_params(p) != HGA_OK || n_seq < 0 || max_q < 0 || n_tok < 0 || max_ctx < 0) return -1;
+  if (n_seq == 0 || max_q == 0 || n_tok == 0) return 0;
+  const int64_t units = (int64_t)n_seq * p->n_kv_heads;
+  const Q4Plan pl = q4_plan(p, units, (int64_t)max_q * (p->n_q_heads / p->n_kv_heads), max_ctx);
+  return q4_work_bytes(p, pl.parts(units), pl.nt);
+}
+
+hga_status hga_q4_attend(const hga_params* p, const hga_page_pool* pool, int32_t plane,
+                         const hga_q4_batch* b, int64_t n_tok, const void* q, int64_t max_ctx,
+                         void* o, float* lse, void* work, int64_t work_bytes,
+                         hga_stream_t stream) {
+  hga::Q4AttendArgs g{};
+  hga_status s = q4_cache(p, pool, plane, &g.c);
+  if (s != HGA_OK) return s;
+  if ((s = check_batch(b, n_tok)) != HGA_OK) return s;
+  if (max_ctx < 0) return HGA_ERR_INVALID_ARG;
+  if (n_tok == 0 || b->n_seq == 0 || b->max_q == 0) return HGA_OK;
+  if (!q || !o || !aligned16(q) || !aligned16(o)) return HGA_ERR_INVALID_ARG;
+  if (b->n_seq > 65535 || p->n_kv_heads > 65535 || n_tok > 0x7fffffff) return HGA_ERR_UNSUPPORTED;
+  const int64_t units = (int64_t)b->n_seq * p->n_kv_heads;
+  const Q4Plan pl = q4_plan(p, units, (int64_t)b->max_q * (p->n_q_heads / p->n_kv_heads), max_ctx);
+  const int64_t need = q4_work_bytes(p, pl.parts(units), pl.nt);
+  if (need > 0 && (!work || !aligned16(work) || work_bytes < need)) return HGA_ERR_INVALID_ARG;
+  g.b = hga::Q4BatchArgs{b->rows, b->off, b->n_seq};
+  g.max_q = b->max_q;
+  g.a.n_q = n_tok;
+  q4_common_args(p, q, o, lse, pl, units, work, &g);
+  return q4_dispatch<false>(p, g, pl, b->n_seq, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int64_t hga_q4_attend_routed_work(const hga_params* p, int64_t n_q) {
+  if (check_params(p) != HGA_OK || n_q < 0) return -1;
+  // units * splits stays below twice the target (q4_plan)
+  return q4_work_bytes(p, 2 * kQ4TargetCtas, 2);
+}
+
+hga_status hga_q4_attend_routed(const hga_params* p, const hga_page_pool* pool, int32_t plane,
+                                int32_t row, const void* q, int64_t q_start, int64_t n_q,
+                                int64_t pos_lo, int64_t t_cap, const int32_t* group_idx,
+                                const int32_t* group_cnt, void* o, float* lse, void* work,
+                                int64_t work_bytes, hga_stream_t stream) {
+  hga::Q4AttendArgs g{};
+  hga_status s = q4_cache(p, pool, plane, &g.c);
+  if (s != HGA_OK) return s;
+  if ((s = check_segment(p, q_start, n_q, t_cap)) != HGA_OK) return s;
+  if (row < 0 || row >= pool->n_rows || pos_lo < q_start) return HGA_ERR_INVALID_ARG;
+  if (q_start + n_q > (int64_t)pool->row_pages * pool->page_tokens) return HGA_ERR_INVALID_ARG;
+  if (pos_lo >= q_start + n_q) return HGA_OK;
+  if (!q || !o || !aligned16(q) || !aligned16(o) || !group_idx || !group_cnt)
+    return HGA_ERR_INVALID_ARG;
+  if (p->n_kv_heads > 65535) return HGA_ERR_UNSUPPORTED;
+  hga::AttendArgs& a = g.a;
+  a.q_start = q_start;
+  a.n_q = n_q;
+  a.group_idx = group_idx;
+  a.group_cnt = group_cnt;
+  a.cap_g = cap_groups(p, t_cap);
+  a.n_blocks = (int)((n_q + p->qblock - 1) / p->qblock);
+  a.group = p->group;
+  a.qblock = p->qblock;
+  a.sink = p->sink;
+  a.local = p->local;
+  a.pos_lo = pos_lo;
+  const int64_t max_list = p->sink / p->group + a.cap_g + p->local / p->group + p->qblock / p->group;
+  if (max_list > 16384) return HGA_ERR_UNSUPPORTED;
+  a.max_list = (int)max_list;
+  g.row = row;
+  g.z0 = (int)((pos_lo - q_start) / p->qblock);
+  const int64_t nz = a.n_blocks - g.z0;
+  const int64_t block_rows = std::min<int64_t>(p->qblock, q_start + n_q - pos_lo);
+  const int64_t units = nz * p->n_kv_heads;
+  const Q4Plan pl = q4_plan(p, units, block_rows * (p->n_q_heads / p->n_kv_heads),
+                            std::min<int64_t>(max_list * 8, q_start + n_q));
+  const int64_t need = q4_work_bytes(p, pl.parts(units), pl.nt);
+  if (need > 0 && (!work || !aligned16(work) || work_bytes < need)) return HGA_ERR_INVALID_ARG;
+  q4_common_args(p, q, o, lse, pl, units, work, &g);
+  return q4_dispatch<true>(p, g, pl, nz, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,307 @@
+// The 4-bit K/V cache: its format, storing tokens and reading them back.
+//
+// 16 neighbouring values of a head share a scale.  The scale is a byte b that
+// stands for the IEEE half with bits b << 7 (5 exponent bits, 3 mantissa bits,
+// no sign): the smallest one with 6 scale >= max|x|, at most 10240 (so that
+// 6 * 10240 = 61440 is still an fp16 value).  A code is 4 bits, sign and
+// magnitude {0, .5, 1, 1.5, 2, 3, 4, 6} (e2m1): the nearest to x / scale, ties
+// to the even code.  A code times a scale has at most 6 significant bits, so
+// the attention's fp16 operands hold it exactly: nothing is rounded after
+// storing.  4.5 bits a value.
+//
+// A record holds 8 tokens of one KV head (the routed attention's group):
+//   K codes [8][d/2], V codes [8][d/2] (dim 2i in the low nibble of byte i),
+//   K scales [8][d/16], V scales [8][d/16]                  = 9 d bytes,
+// one contiguous span whose size is a multiple of 16 bytes, so one bulk copy
+// fetches a group's K and V.  A page is [KV head][page_tokens / 8] records: a
+// head's tokens of a page are contiguous too.
+#pragma once
+#include <cuda_fp16.h>
+#include "common.cuh"
+
+namespace hga {
+
+constexpr int kQ4MaxScale = 226;            // the byte of 10240
+constexpr float kQ4MaxValue = 61440.0f;
+
+__host__ __device__ constexpr int q4_record_bytes(int d) { return 9 * d; }
+
+struct Q4Cache {
+  char* base;                // the plane's pages
+  int64_t page_bytes;
+  const int32_t* table;      // [n_rows][row_pages]
+  const int32_t* len;        // [n_rows]
+  int n_pages, n_rows, row_pages, page_recs, page_tokens, Hkv;
+};
+
+struct Q4BatchArgs {
+  const int32_t* rows;       // [n_seq] table rows, < 0 = inactive
+  const int32_t* off;        // [n_seq + 1], null: one token each
+  int n_seq;
+};
+
+// Where a token of the batch lives: its table row and position; false where
+// it belongs to no sequence (behind the last one, or an inactive one).
+__device__ __forceinline__ bool q4_locate(const Q4Cache& c, const Q4BatchArgs& b, int64_t tok,
+                                          int* row, int* pos) {
+  int s, n, j;
+  if (b.off) {
+    // last sequence whose start is at or before the token
+    int lo = 0, hi = b.n_seq;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (b.off[mid + 1] <= tok) lo = mid + 1;
+      else hi = mid;
+    }
+    s = lo;
+    if (s >= b.n_seq) return false;
+    const int o = b.off[s];
+    if (tok < o) return false;
+    n = b.off[s + 1] - o;
+    j = (int)(tok - o);
+  } else {
+    if (tok >= b.n_seq) return false;
+    s = (int)tok;
+    n = 1;
+    j = 0;
+  }
+  const int r = b.rows[s];
+  if (r < 0) return false;
+  if (r >= c.n_rows) {
+    report(HGA_ERR_DEVICE_CHECK);
+    return false;
+  }
+  *row = r;
+  *pos = c.len[r] - n + j;
+  return true;
+}
+
+// The record of (row, position, head), or null (reported) where the page table
+// names none.
+__device__ __forceinline__ char* q4_record(const Q4Cache& c, int row, int pos, int h, int rec) {
+  if (pos < 0 || pos >= (int64_t)c.row_pages * c.page_tokens) {
+    report(HGA_ERR_DEVICE_CHECK);
+    return nullptr;
+  }
+  const int col = pos / c.page_tokens;
+  const int pg = c.table[(int64_t)row * c.row_pages + col];
+  if (pg < 0 || pg >= c.n_pages) {
+    report(HGA_ERR_DEVICE_CHECK);
+    return nullptr;
+  }
+  const int in = (pos - col * c.page_tokens) >> 3;
+  return c.base + pg * c.page_bytes + ((int64_t)h * c.page_recs + in) * rec;
+}
+
+__device__ __forceinline__ float q4_scale(int b) {
+  return __half2float(__ushort_as_half((unsigned short)(b << 7)));
+}
+
+// Smallest scale byte with 6 scale >= m (m >= 0, finite).
+__device__ __forceinline__ int q4_scale_byte(float m) {
+  m = fminf(m, kQ4MaxValue);
+  // a first guess from m / 6 rounded up to 4 significant bits, then exact
+  // comparisons (6 scale has 5 significant bits)
+  int b = (__half_as_ushort(__float2half_ru(m * 0.16666667f)) + 127) >> 7;
+  b = min(b, kQ4MaxScale);
+  while (b > 0 && 6.0f * q4_scale(b - 1) >= m) --b;
+  while (b < kQ4MaxScale && 6.0f * q4_scale(b) < m) ++b;
+  return b;
+}
+
+// Codes of two values already divided by their scale (first one in the low nibble).
+__device__ __forceinline__ uint32_t q4_code2(float lo, float hi) {
+  uint32_t r;
+  asm("{\n .reg .b8 c;\n cvt.rn.satfinite.e2m1x2.f32 c, %1, %2;\n"
+      " mov.b32 %0, {c, 0, 0, 0};\n}\n"
+      : "=r"(r)
+      : "f"(hi), "f"(lo));
+  return r;
+}
+
+// x / s, exact where the quotient is a tie of the code grid.  For fp32 inputs a
+// correctly rounded quotient is enough: x has 24 bits and s 4, so a quotient
+// that is no tie lies more than half an ulp of the tie away from it.  bf16
+// inputs go through a product with 1/s, whose error (2^-23) is taken off by
+// rounding to a multiple of 2^-12: |x / s - tie| is 0 or at least 2^-10.
+template <typename T>
+__device__ __forceinline__ float q4_ratio(float x, float s, float inv) {
+  if constexpr (sizeof(T) == 4) return __fdiv_rn(x, s);
+  return (x * inv + 2048.0f) - 2048.0f;
+}
+
+// 16 values -> 8 code bytes and the scale byte.
+template <typename T>
+__device__ __forceinline__ uint2 q4_encode(const float* f, int* scale, bool* bad) {
+  float m = 0.f;
+  bool over = false;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    m = fmaxf(m, fabsf(f[i]));
+    over |= !(fabsf(f[i]) <= kQ4MaxValue);     // NaN too
+  }
+  *bad |= over;
+  const int b = q4_scale_byte(m);
+  *scale = b;
+  if (b == 0) return make_uint2(0, 0);
+  const float s = q4_scale(b), inv = 1.0f / s;
+  uint32_t w[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float x = f[2 * i], y = f[2 * i + 1];
+    if (over) {
+      x = x == x ? fminf(fmaxf(x, -kQ4MaxValue), kQ4MaxValue) : 0.f;
+      y = y == y ? fminf(fmaxf(y, -kQ4MaxValue), kQ4MaxValue) : 0.f;
+    }
+    w[i >> 2] |= q4_code2(q4_ratio<T>(x, s, inv), q4_ratio<T>(y, s, inv)) << (8 * (i & 3));
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+// Eight codes (one word) -> four pairs of fp16.
+__device__ __forceinline__ void q4_unpack8(uint32_t w, uint32_t* h) {
+  asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %4;\n"
+      " cvt.rn.f16x2.e2m1x2 %0, a;\n cvt.rn.f16x2.e2m1x2 %1, b;\n"
+      " cvt.rn.f16x2.e2m1x2 %2, c;\n cvt.rn.f16x2.e2m1x2 %3, d;\n}\n"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+__device__ __forceinline__ uint32_t q4_mul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// ---------------------------------------------------------------- append
+
+constexpr int kQ4Threads = 256;
+
+struct Q4IoArgs {
+  Q4Cache c;
+  Q4BatchArgs b;
+  const void *k, *v;         // append: the tokens; read: where they go
+  int64_t k_tok, k_head, v_tok, v_head;   // strides in elements
+  int64_t n_tok;
+  int D;
+};
+
+template <typename T>
+__device__ __forceinline__ void q4_load16(const T* p, float* f) {
+  if constexpr (sizeof(T) == 2) {
+    const uint4 r[2] = {reinterpret_cast<const uint4*>(p)[0], reinterpret_cast<const uint4*>(p)[1]};
+    const uint32_t w[8] = {r[0].x, r[0].y, r[0].z, r[0].w, r[1].x, r[1].y, r[1].z, r[1].w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 r = reinterpret_cast<const float4*>(p)[i];
+      f[4 * i] = r.x; f[4 * i + 1] = r.y; f[4 * i + 2] = r.z; f[4 * i + 3] = r.w;
+    }
+  }
+}
+
+// One thread per 16 values of K and the same 16 of V: the maximum needs no
+// exchange between threads.  Bound: HBM (reads 4 d, writes 9 d / 8 bytes per
+// token and head).
+template <typename T>
+__global__ void __launch_bounds__(kQ4Threads) q4_append_kernel(const Q4IoArgs a) {
+  griddep_wait();
+  const int nb = a.D >> 4;                          // scale blocks of a head's row
+  const int64_t total = a.n_tok * a.c.Hkv * nb;
+  bool bad = false;
+  // a row named by two sequences of the call would be written twice: reported
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i < a.b.n_seq; i += kQ4Threads)
+      for (int j = 0; j < i; ++j)
+        if (a.b.rows[i] >= 0 && a.b.rows[j] == a.b.rows[i]) bad = true;
+  for (int64_t i = (int64_t)blockIdx.x * kQ4Threads + threadIdx.x; i < total;
+       i += (int64_t)gridDim.x * kQ4Threads) {
+    const int blk = (int)(i % nb);
+    const int64_t th = i / nb;
+    const int h = (int)(th % a.c.Hkv);
+    const int64_t tok = th / a.c.Hkv;
+    int row, pos;
+    if (!q4_locate(a.c, a.b, tok, &row, &pos)) continue;
+    char* rec = q4_record(a.c, row, pos, h, q4_record_bytes(a.D));
+    if (!rec) continue;
+    const int r = pos & 7;
+    float k[16], v[16];
+    q4_load16(static_cast<const T*>(a.k) + tok * a.k_tok + h * a.k_head + blk * 16, k);
+    q4_load16(static_cast<const T*>(a.v) + tok * a.v_tok + h * a.v_head + blk * 16, v);
+    int ks, vs;
+    const uint2 kc = q4_encode<T>(k, &ks, &bad);
+    const uint2 vc = q4_encode<T>(v, &vs, &bad);
+    const int half = a.D >> 1;
+    *reinterpret_cast<uint2*>(rec + r * half + blk * 8) = kc;
+    *reinterpret_cast<uint2*>(rec + 8 * half + r * half + blk * 8) = vc;
+    rec[16 * half + r * nb + blk] = (char)ks;
+    rec[16 * half + 8 * nb + r * nb + blk] = (char)vs;
+  }
+  if (bad) report(HGA_ERR_DEVICE_CHECK);
+  griddep_launch();
+}
+
+// ---------------------------------------------------------------- read
+
+// The batch's tokens back as the values their codes stand for, in TK and TV
+// (exact in bf16, fp16 and fp32).
+template <typename T>
+__device__ __forceinline__ void q4_decode16(const uint2 codes, int scale, T* out) {
+  const uint32_t s2 = (uint32_t)(scale << 7) * 0x10001u;
+  uint32_t h[8];
+  q4_unpack8(codes.x, h);
+  q4_unpack8(codes.y, h + 4);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) h[i] = q4_mul2(h[i], s2);
+  if constexpr (sizeof(T) == 2) {
+    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<__half2*>(&h[i]));
+        const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
+        h[i] = *reinterpret_cast<const uint32_t*>(&b);
+      }
+    }
+    reinterpret_cast<uint4*>(out)[0] = make_uint4(h[0], h[1], h[2], h[3]);
+    reinterpret_cast<uint4*>(out)[1] = make_uint4(h[4], h[5], h[6], h[7]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(*reinterpret_cast<__half2*>(&h[2 * i]));
+      const float2 g = __half22float2(*reinterpret_cast<__half2*>(&h[2 * i + 1]));
+      reinterpret_cast<float4*>(out)[i] = make_float4(f.x, f.y, g.x, g.y);
+    }
+  }
+}
+
+template <typename TK, typename TV>
+__global__ void __launch_bounds__(kQ4Threads) q4_read_kernel(const Q4IoArgs a) {
+  griddep_wait();
+  const int nb = a.D >> 4, half = a.D >> 1;
+  const int64_t total = a.n_tok * a.c.Hkv * nb;
+  for (int64_t i = (int64_t)blockIdx.x * kQ4Threads + threadIdx.x; i < total;
+       i += (int64_t)gridDim.x * kQ4Threads) {
+    const int blk = (int)(i % nb);
+    const int64_t th = i / nb;
+    const int h = (int)(th % a.c.Hkv);
+    const int64_t tok = th / a.c.Hkv;
+    int row, pos;
+    if (!q4_locate(a.c, a.b, tok, &row, &pos)) continue;
+    const char* rec = q4_record(a.c, row, pos, h, q4_record_bytes(a.D));
+    if (!rec) continue;
+    const int r = pos & 7;
+    const uint2 kc = *reinterpret_cast<const uint2*>(rec + r * half + blk * 8);
+    const uint2 vc = *reinterpret_cast<const uint2*>(rec + 8 * half + r * half + blk * 8);
+    const int ks = (unsigned char)rec[16 * half + r * nb + blk];
+    const int vs = (unsigned char)rec[16 * half + 8 * nb + r * nb + blk];
+    q4_decode16(kc, ks, (TK*)a.k + tok * a.k_tok + h * a.k_head + blk * 16);
+    q4_decode16(vc, vs, (TV*)a.v + tok * a.v_tok + h * a.v_head + blk * 16);
+  }
+  griddep_launch();
+}
+
+}  // namespace hga

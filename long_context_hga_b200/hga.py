@@ -35,7 +35,11 @@ EXPORTED = ("hga_build_summaries", "hga_route_chunks", "hga_route_groups",
             "hga_store_attach_cache", "hga_store_append", "hga_store_set_length",
             "hga_store_length", "hga_store_page_bytes", "hga_store_pages_per_head",
             "hga_store_read", "hga_store_prepare", "hga_gather_store", "hga_forward_causal",
-            "hga_set_wait_limit_ns", "hga_selftest_wait", "hga_debug_stall_next_attend")
+            "hga_set_wait_limit_ns", "hga_selftest_wait", "hga_debug_stall_next_attend",
+            "hga_rope", "hga_rope_backward", "hga_pages_work_ints", "hga_pages_reserve",
+            "hga_pages_fork", "hga_pages_free", "hga_pages_compact", "hga_pages_copy",
+            "hga_q4_page_bytes", "hga_q4_append", "hga_q4_read", "hga_q4_attend",
+            "hga_q4_attend_work", "hga_q4_attend_routed", "hga_q4_attend_routed_work")
 
 
 class HgaError(RuntimeError):
@@ -668,3 +672,389 @@ def store_step(p: Params, q, q_start: int, tier: HostTier, store: KVStore, k_dev
     attend(p, q, q_start, k_dev, v_dev, bufs.group_idx, bufs.group_cnt, bufs.o, bufs.lse)
     install_group_cache(p, t_cap, tier)
     return stats
+
+
+# ---------------------------------------------------------------- rotary positions
+
+class CRopePlan(ctypes.Structure):
+    _fields_ = [("freq", ctypes.c_void_p), ("axis", ctypes.c_void_p)] + [
+        (n, ctypes.c_int32) for n in ("n_axes", "head_dim", "rot_dim", "adjacent")]
+
+
+class CRopeIo(ctypes.Structure):
+    _fields_ = [("in_", ctypes.c_void_p), ("out", ctypes.c_void_p)] + [
+        (n, ctypes.c_int64) for n in ("in_token_stride", "in_head_stride", "out_token_stride",
+                                      "out_head_stride")] + [
+        (n, ctypes.c_int32) for n in ("heads", "in_dtype", "out_dtype")]
+
+
+class CPagePool(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("page_bytes", ctypes.c_int64),
+                ("plane_stride", ctypes.c_int64)] + [
+        (n, ctypes.c_int32) for n in ("n_pages", "n_planes", "page_tokens", "n_rows",
+                                      "row_pages")] + [
+        (n, ctypes.c_void_p) for n in ("table", "len", "ref", "work")]
+
+
+class CQ4Batch(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_void_p), ("off", ctypes.c_void_p), ("n_seq", ctypes.c_int32),
+                ("max_q", ctypes.c_int32)]
+
+
+def _sig_serving():
+    P, R, IO = (ctypes.POINTER(c) for c in (CParams, CRopePlan, CRopeIo))
+    G, B = ctypes.POINTER(CPagePool), ctypes.POINTER(CQ4Batch)
+    vp, i64, i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
+    st = ctypes.c_int
+    sig = {
+        "hga_rope": (st, [R, vp, i64, i64, IO, IO, vp]),
+        "hga_rope_backward": (st, [R, vp, i64, i64, IO, IO, vp]),
+        "hga_pages_work_ints": (i64, [G]),
+        "hga_pages_reserve": (st, [G, vp, vp, i32, vp]),
+        "hga_pages_fork": (st, [G, vp, vp, i32, vp]),
+        "hga_pages_free": (st, [G, vp, i32, vp]),
+        "hga_pages_compact": (st, [G, vp]),
+        "hga_pages_copy": (st, [G, vp, vp, i32, vp]),
+        "hga_q4_page_bytes": (i64, [P, i32]),
+        "hga_q4_append": (st, [P, G, i32, B, i64, vp, i64, i64, vp, i64, i64, vp]),
+        "hga_q4_read": (st, [P, G, i32, B, i64, vp, i64, i64, vp, i64, i64, vp]),
+        "hga_q4_attend": (st, [P, G, i32, B, i64, vp, i64, vp, vp, vp, i64, vp]),
+        "hga_q4_attend_work": (i64, [P, i32, i32, i64, i64]),
+        "hga_q4_attend_routed": (st, [P, G, i32, i32, vp, i64, i64, i64, i64, vp, vp, vp, vp, vp,
+                                      i64, vp]),
+        "hga_q4_attend_routed_work": (i64, [P, i64]),
+    }
+    for name, (ret, args) in sig.items():
+        fn = getattr(LIB, name)
+        fn.restype = ret
+        fn.argtypes = args
+
+
+_sig_serving()
+
+_RAW_STREAM = torch._C._cuda_getCurrentRawStream
+
+
+def _on(what: str, stream, *tensors) -> int:
+    """The raw stream of a call whose tensors (None is skipped) must all be on
+    the current CUDA device; HgaError otherwise."""
+    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise HgaError(HGA_ERR_INVALID_ARG, f"{what}: tensors must be on the current CUDA device")
+    return _RAW_STREAM(dev) if stream is None else stream.cuda_stream
+
+
+def _want(ok: bool, what: str):
+    if not ok:
+        raise HgaError(HGA_ERR_INVALID_ARG, what)
+
+
+def _cp(p: Params):
+    """The C struct of a Params, built once (Params is immutable)."""
+    c = p.__dict__.get("_c")
+    if c is None:
+        c = p.c()
+        object.__setattr__(p, "_c", c)
+    return ctypes.byref(c)
+
+
+_ROPE_DTYPES = {torch.bfloat16: HGA_BF16, torch.float32: HGA_FP32}
+
+
+class Rope:
+    """A rotary plan: freq (float64 [rot_dim/2], radians per position) and axis
+    (uint8 [rot_dim/2], the axis whose position turns each pair) on the device.
+    adjacent: pairs are (2i, 2i + 1) instead of (i, i + rot_dim/2)."""
+
+    def __init__(self, freq: torch.Tensor, axis: torch.Tensor, head_dim: int,
+                 n_axes: Optional[int] = None, adjacent: bool = False):
+        _want(freq.dtype == torch.float64 and freq.dim() == 1 and freq.is_contiguous(),
+              "Rope: freq is a float64 vector")
+        _want(axis.dtype == torch.uint8 and axis.shape == freq.shape and axis.is_contiguous(),
+              "Rope: axis is a uint8 vector of freq's length")
+        _want(0 <= 2 * freq.numel() <= head_dim, "Rope: more pairs than head_dim has")
+        self.freq, self.axis, self.head_dim, self.adjacent = freq, axis, head_dim, adjacent
+        if n_axes is None:
+            n_axes = int(axis.max()) + 1 if axis.numel() else 1
+        self.n_axes = n_axes
+        self._c = CRopePlan(freq.data_ptr(), axis.data_ptr(), n_axes, head_dim, 2 * freq.numel(),
+                            int(adjacent))
+
+    @staticmethod
+    def make(head_dim: int, theta: float, sections=None, rot_dim: Optional[int] = None,
+             interleaved: bool = False, adjacent: bool = False, device="cuda") -> "Rope":
+        """Frequencies theta^(-2i/rot_dim).  sections: how many pairs each axis
+        takes (their sum is rot_dim/2; default: one axis), in runs, or dealt out
+        in turn (interleaved: pair i goes to axis i mod n while that axis has
+        pairs left)."""
+        rot_dim = head_dim if rot_dim is None else rot_dim
+        half = rot_dim // 2
+        sections = [half] if sections is None else list(sections)
+        _want(sum(sections) == half and min(sections) >= 0,
+              "Rope.make: sections must add up to rot_dim / 2")
+        if interleaved:
+            left, axis = list(sections), []
+            while len(axis) < half:
+                for a in range(len(left)):
+                    if left[a] > 0:
+                        left[a] -= 1
+                        axis.append(a)
+        else:
+            axis = [a for a, n in enumerate(sections) for _ in range(n)]
+        freq = theta ** (-torch.arange(half, dtype=torch.float64) * 2 / max(rot_dim, 1))
+        return Rope(freq.to(device), torch.tensor(axis, dtype=torch.uint8, device=device),
+                    head_dim, n_axes=len(sections), adjacent=adjacent)
+
+
+def _rope_io(what: str, n: int, d: int, x, out):
+    _want(x.dim() == 3 and x.shape == out.shape and x.shape[0] == n and x.shape[2] == d
+          and (x.stride(2) == 1 or d == 1) and (out.stride(2) == 1 or d == 1),
+          f"{what}: tensors are [n, heads, head_dim] with contiguous heads")
+    _want(x.dtype in _ROPE_DTYPES and out.dtype in _ROPE_DTYPES, f"{what}: bf16 or fp32")
+    return CRopeIo(x.data_ptr(), out.data_ptr(), x.stride(0), x.stride(1), out.stride(0),
+                   out.stride(1), x.shape[1], _ROPE_DTYPES[x.dtype], _ROPE_DTYPES[out.dtype])
+
+
+def _rope(what: str, fn, plan: Rope, pos, q, q_out, k, k_out, stream):
+    if pos.dim() == 1:
+        pos = pos.unsqueeze(0)
+    n = q.shape[0]
+    _want(pos.dtype == torch.int32 and pos.shape[0] >= plan.n_axes and pos.shape[1] == n
+          and (n <= 1 or pos.stride(1) == 1), f"{what}: pos is int32 [n_axes, n]")
+    _want((k is None) == (k_out is None), f"{what}: k and k_out come together")
+    st = _on(what, stream, plan.freq, pos, q, q_out, k, k_out)
+    if k is not None:
+        _want(k.dtype == q.dtype and k_out.dtype == q_out.dtype, f"{what}: q and k have one dtype")
+    io = _rope_io(what, n, plan.head_dim, q, q_out)
+    kio = None if k is None else ctypes.byref(_rope_io(what, n, plan.head_dim, k, k_out))
+    stride = pos.stride(0) if pos.shape[0] > 1 else n
+    _ok(fn(ctypes.byref(plan._c), pos.data_ptr(), stride, n, ctypes.byref(io), kio, st), what)
+
+
+def rope(plan: Rope, pos, q, q_out, k=None, k_out=None, stream=None):
+    """Rotates q [n, Hq, d] into q_out and k [n, Hkv, d] into k_out at the
+    positions pos (int32 [n_axes, n]; [n] for one axis).  Any token and head
+    strides: q and k may be views of a fused projection, k_out the view
+    cache[:, t0:t0 + n].transpose(0, 1) of a [Hkv, t_cap, d] cache; out may be
+    the input itself."""
+    _rope("hga_rope", LIB.hga_rope, plan, pos, q, q_out, k, k_out, stream)
+
+
+def rope_backward(plan: Rope, pos, d_q, d_q_out, d_k=None, d_k_out=None, stream=None):
+    """Gradients of rope's inputs from those of its outputs (any strides, bf16
+    or fp32 on either side: attend_backward's fp32 d_q and d_k go straight in)."""
+    _rope("hga_rope_backward", LIB.hga_rope_backward, plan, pos, d_q, d_q_out, d_k, d_k_out,
+          stream)
+
+
+# ---------------------------------------------------------------- pages of a cache
+
+class PagePool:
+    """A pool of pages and the table of the sequences that use them.
+    data: uint8 [n_planes, n_pages, page_bytes] (plane = layer), table: int32
+    [n_rows, row_pages] (-1 = none), length: int32 [n_rows], ref: int32
+    [n_pages], all on one device, changed in place by the pages_* and q4_* calls."""
+
+    def __init__(self, data: torch.Tensor, table: torch.Tensor, length: torch.Tensor,
+                 ref: torch.Tensor, page_tokens: int):
+        _want(data.dtype == torch.uint8 and data.dim() == 3 and data.stride(2) == 1
+              and (data.shape[1] == 1 or data.stride(1) == data.shape[2]),
+              "PagePool: data is uint8 [n_planes, n_pages, page_bytes]")
+        for t, shape in ((table, table.shape), (length, table.shape[:1]), (ref, data.shape[1:2])):
+            _want(t.dtype == torch.int32 and t.is_contiguous() and t.shape == shape
+                  and t.device == data.device, "PagePool: table, length and ref are int32")
+        _want(table.dim() == 2, "PagePool: table is [n_rows, row_pages]")
+        self.data, self.table, self.length, self.ref = data, table, length, ref
+        self.page_tokens = page_tokens
+        stride = data.stride(0) if data.shape[0] > 1 else data.shape[1] * data.shape[2]
+        self._c = CPagePool(data.data_ptr(), data.shape[2], stride, data.shape[1], data.shape[0],
+                            page_tokens, table.shape[0], table.shape[1], table.data_ptr(),
+                            length.data_ptr(), ref.data_ptr(), None)
+        words = LIB.hga_pages_work_ints(ctypes.byref(self._c))
+        _want(words > 0, "PagePool: sizes")
+        self.work = torch.zeros(words, dtype=torch.int32, device=data.device)
+        self._c.work = self.work.data_ptr()
+        self._r = ctypes.byref(self._c)
+
+    @staticmethod
+    def allocate(n_planes: int, n_pages: int, page_bytes: int, page_tokens: int, n_rows: int,
+                 row_pages: int, device="cuda") -> "PagePool":
+        """An empty pool: every page free, every row empty."""
+        i32 = torch.int32
+        return PagePool(
+            torch.empty(n_planes, n_pages, page_bytes, dtype=torch.uint8, device=device),
+            torch.full((n_rows, row_pages), -1, dtype=i32, device=device),
+            torch.zeros(n_rows, dtype=i32, device=device),
+            torch.zeros(n_pages, dtype=i32, device=device), page_tokens)
+
+
+def _list(what: str, *lists):
+    n = lists[0].numel()
+    for x in lists:
+        _want(x.dtype == torch.int32 and x.dim() == 1 and x.is_contiguous() and x.numel() == n,
+              f"{what}: lists are int32 vectors of one length")
+    return n
+
+
+def pages_reserve(pool: PagePool, rows, new_len, stream=None):
+    """Row rows[i] grows to new_len[i] tokens (lowest free pages first)."""
+    n = _list("hga_pages_reserve", rows, new_len)
+    st = _on("hga_pages_reserve", stream, pool.data, rows, new_len)
+    _ok(LIB.hga_pages_reserve(pool._r, rows.data_ptr(), new_len.data_ptr(), n, st),
+        "hga_pages_reserve")
+
+
+def pages_fork(pool: PagePool, parents, children, stream=None):
+    """Empty rows children[i] become copies of rows parents[i]: whole pages are
+    shared, a last page that ends inside is copied."""
+    n = _list("hga_pages_fork", parents, children)
+    st = _on("hga_pages_fork", stream, pool.data, parents, children)
+    _ok(LIB.hga_pages_fork(pool._r, parents.data_ptr(), children.data_ptr(), n, st),
+        "hga_pages_fork")
+
+
+def pages_free(pool: PagePool, rows, stream=None):
+    """Returns the rows' pages and empties the rows."""
+    n = _list("hga_pages_free", rows)
+    st = _on("hga_pages_free", stream, pool.data, rows)
+    _ok(LIB.hga_pages_free(pool._r, rows.data_ptr(), n, st), "hga_pages_free")
+
+
+def pages_compact(pool: PagePool, stream=None):
+    """Moves the used pages to the front of the pool."""
+    st = _on("hga_pages_compact", stream, pool.data)
+    _ok(LIB.hga_pages_compact(pool._r, st), "hga_pages_compact")
+
+
+def pages_copy(pool: PagePool, src, dst, stream=None):
+    """Copies pages src[i] to dst[i] in every plane."""
+    n = _list("hga_pages_copy", src, dst)
+    st = _on("hga_pages_copy", stream, pool.data, src, dst)
+    _ok(LIB.hga_pages_copy(pool._r, src.data_ptr(), dst.data_ptr(), n, st), "hga_pages_copy")
+
+
+# ---------------------------------------------------------------- 4-bit K/V cache
+
+class Q4Batch:
+    """The sequences of a call: table rows (int32 [n_seq], negative =
+    inactive), off (int32 [n_seq + 1], each sequence's span of the packed tokens; None:
+    one token each) and max_q, the most tokens of a sequence."""
+
+    def __init__(self, rows: torch.Tensor, off: Optional[torch.Tensor] = None, max_q: int = 1):
+        _list("Q4Batch", rows)
+        if off is not None:
+            _list("Q4Batch", off)
+            _want(off.numel() == rows.numel() + 1, "Q4Batch: off is [n_seq + 1]")
+        self.rows, self.off, self.max_q = rows, off, max_q
+        self._c = CQ4Batch(rows.data_ptr(), None if off is None else off.data_ptr(), rows.numel(),
+                           max_q)
+        self._r = ctypes.byref(self._c)
+
+
+def q4_page_bytes(p: Params, page_tokens: int) -> int:
+    """Bytes of a page of page_tokens tokens (all KV heads, K and V)."""
+    n = LIB.hga_q4_page_bytes(_cp(p), page_tokens)
+    _want(n > 0, "hga_q4_page_bytes")
+    return n
+
+
+def _q4_kv(what: str, p: Params, n: int, k, v, v_dtype):
+    shape = (n, p.n_kv_heads, p.head_dim)
+    _want(k.shape == shape and v.shape == shape and k.stride(2) == 1 and v.stride(2) == 1,
+          f"{what}: k and v are [n_tok, n_kv_heads, head_dim] with contiguous heads")
+    _want(k.dtype == p.torch_dtype and v.dtype == v_dtype, f"{what}: dtype")
+
+
+def q4_append(p: Params, pool: PagePool, plane: int, batch: Q4Batch, k, v, stream=None):
+    """Stores the batch's tokens: k, v [n_tok, Hkv, d] (any token and head
+    strides), the last tokens of their rows (grow them with pages_reserve)."""
+    n = k.shape[0]
+    _q4_kv("hga_q4_append", p, n, k, v, p.torch_dtype)
+    st = _on("hga_q4_append", stream, pool.data, batch.rows, k, v)
+    _ok(LIB.hga_q4_append(_cp(p), pool._r, plane, batch._r, n, k.data_ptr(), k.stride(0),
+                          k.stride(1), v.data_ptr(), v.stride(0), v.stride(1), st),
+        "hga_q4_append")
+
+
+def q4_read(p: Params, pool: PagePool, plane: int, batch: Q4Batch, k, v, stream=None):
+    """Reads the batch's tokens back into k and v [n_tok, Hkv, d] (any strides,
+    such as a [Hkv, t_cap, d] buffer's; v in fp16 with p.v_f16)."""
+    n = k.shape[0]
+    _q4_kv("hga_q4_read", p, n, k, v, torch.float16 if p.v_f16 else p.torch_dtype)
+    st = _on("hga_q4_read", stream, pool.data, batch.rows, k, v)
+    _ok(LIB.hga_q4_read(_cp(p), pool._r, plane, batch._r, n, k.data_ptr(), k.stride(0),
+                        k.stride(1), v.data_ptr(), v.stride(0), v.stride(1), st), "hga_q4_read")
+
+
+def _work(n_bytes: int, device, stream):
+    w = torch.empty(n_bytes, dtype=torch.uint8, device=device)
+    if stream is not None:
+        w.record_stream(stream)
+    return w
+
+
+def q4_workspace(p: Params, batch: Q4Batch, n_tok: int, max_ctx: int) -> Optional[torch.Tensor]:
+    """Workspace of q4_attend calls of this size, one at a time (None: none needed)."""
+    n = LIB.hga_q4_attend_work(_cp(p), batch.rows.numel(), batch.max_q, n_tok, max_ctx)
+    _want(n >= 0, "hga_q4_attend_work")
+    return _work(n, batch.rows.device, None) if n else None
+
+
+def q4_routed_workspace(p: Params, n_q: int, device="cuda") -> Optional[torch.Tensor]:
+    """Workspace of q4_attend_routed calls of n_q queries, one at a time."""
+    n = LIB.hga_q4_attend_routed_work(_cp(p), n_q)
+    _want(n >= 0, "hga_q4_attend_routed_work")
+    return _work(n, device, None) if n else None
+
+
+def _q4_out(what: str, p: Params, q, o, lse):
+    _want(q.dim() == 3 and q.shape[1] == p.n_q_heads and q.shape[2] == p.head_dim
+          and q.dtype == p.torch_dtype and q.is_contiguous() and o.shape == q.shape
+          and o.dtype == q.dtype and o.is_contiguous(), f"{what}: q and o are [n, Hq, d]")
+    _want(lse is None or (lse.dtype == torch.float32 and lse.shape == q.shape[:2]
+                          and lse.is_contiguous()), f"{what}: lse is float32 [n, Hq]")
+
+
+def q4_attend(p: Params, pool: PagePool, plane: int, batch: Q4Batch, q, o, lse=None,
+              max_ctx: Optional[int] = None, work=None, stream=None):
+    """Dense causal attention of the batch's tokens q [n_tok, Hq, d] over their
+    rows' tokens.  max_ctx bounds the rows' lengths (default: the table's
+    capacity); work: q4_workspace(...) of the caller (default: allocated here)."""
+    n = q.shape[0]
+    _q4_out("hga_q4_attend", p, q, o, lse)
+    st = _on("hga_q4_attend", stream, pool.data, batch.rows, q, o, lse, work)
+    if max_ctx is None:
+        max_ctx = pool.table.shape[1] * pool.page_tokens
+    if work is None:
+        need = LIB.hga_q4_attend_work(_cp(p), batch.rows.numel(), batch.max_q, n, max_ctx)
+        work = _work(need, q.device, stream) if need > 0 else None
+    _ok(LIB.hga_q4_attend(_cp(p), pool._r, plane, batch._r, n, q.data_ptr(), max_ctx,
+                          o.data_ptr(), None if lse is None else lse.data_ptr(),
+                          None if work is None else work.data_ptr(),
+                          0 if work is None else work.numel() * work.element_size(), st),
+        "hga_q4_attend")
+
+
+def q4_attend_routed(p: Params, pool: PagePool, plane: int, row: int, q, q_start: int, t_cap: int,
+                     group_idx, group_cnt, o, lse=None, pos_lo: Optional[int] = None, work=None,
+                     stream=None):
+    """attend with K and V in table row `row` of the pool.  pos_lo: rows of
+    earlier positions are left as they are (default q_start: none)."""
+    n = q.shape[0]
+    _q4_out("hga_q4_attend_routed", p, q, o, lse)
+    nb = (n + p.qblock - 1) // p.qblock
+    _want(group_idx.dtype == torch.int32 and group_cnt.dtype == torch.int32
+          and group_idx.is_contiguous() and group_cnt.is_contiguous()
+          and group_cnt.shape == (p.n_kv_heads, nb)
+          and group_idx.shape == (p.n_kv_heads, nb, max(index_capacity(p, t_cap, 1), 1)),
+          "hga_q4_attend_routed: group_idx and group_cnt as allocate(p, t_cap, n_q) makes them")
+    st = _on("hga_q4_attend_routed", stream, pool.data, q, o, lse, group_idx, group_cnt, work)
+    if work is None:
+        work = _work(LIB.hga_q4_attend_routed_work(_cp(p), n), q.device, stream)
+    _ok(LIB.hga_q4_attend_routed(_cp(p), pool._r, plane, row, q.data_ptr(), q_start, n,
+                                 q_start if pos_lo is None else pos_lo, t_cap,
+                                 group_idx.data_ptr(), group_cnt.data_ptr(), o.data_ptr(),
+                                 None if lse is None else lse.data_ptr(), work.data_ptr(),
+                                 work.numel() * work.element_size(), st),
+        "hga_q4_attend_routed")
