@@ -26,6 +26,7 @@
 #include "pages.cuh"
 #include "q4.cuh"
 #include "q4_attend.cuh"
+#include "q4_attend_tc.cuh"
 
 namespace {
 
@@ -73,7 +74,9 @@ hga_status launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t sm
 // belongs to the device context).
 constexpr size_t kMaxSmemPerBlock = 227 * 1024;
 
-template <auto kernel>
+// kRegs: registers a thread that the kernel's own split of them (setmaxnreg)
+// adds up to; a build that gives it fewer at launch is refused.
+template <auto kernel, int kRegs = 0>
 hga_status allow_smem(size_t bytes) {
   static std::atomic<uint64_t> done{0};
   static std::atomic<size_t> dyn_max{0};
@@ -84,6 +87,7 @@ hga_status allow_smem(size_t bytes) {
   if (!(done.load(std::memory_order_acquire) & bit)) {
     cudaFuncAttributes fa;
     if ((e = cudaFuncGetAttributes(&fa, kernel)) != cudaSuccess) return cuda_ok(e);
+    if (fa.numRegs < kRegs) return HGA_ERR_UNSUPPORTED;
     const size_t avail = kMaxSmemPerBlock - fa.sharedSizeBytes;
     if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   (int)avail)) != cudaSuccess)
@@ -1220,27 +1224,56 @@ unsigned q4_io_grid(const hga::Q4IoArgs& a) {
 
 // ---------------------------------------------------------------- 4-bit attention
 
-// How a call is cut: rows per tile, tiles of a unit, CTAs per unit and tile.
+// How a call is cut: the kernel, rows per tile, tiles of a unit, CTAs per unit
+// and tile.
 struct Q4Plan {
-  int nt = 1, n_tiles = 1, n_split = 1;
+  bool tc = false;
+  int rows = 8, n_tiles = 1, n_split = 1;
   int64_t parts(int64_t units) const { return n_split > 1 ? units * n_tiles * n_split : 0; }
 };
 
 constexpr int64_t kQ4TargetCtas = 148 * 4;
+constexpr int64_t kQ4TcMinRows = 64;
 
-Q4Plan q4_plan(const hga_params* p, int64_t units, int64_t rows, int64_t max_tok) {
+// rows, max_tok: most query rows and tokens of a unit.
+Q4Plan q4_plan(const hga_params* p, int64_t units, int64_t rows, int64_t max_tok, int max_list) {
   Q4Plan pl;
-  pl.nt = p->dtype == HGA_BF16 && rows > 8 ? 2 : 1;
-  pl.n_tiles = (int)((rows + 8 * pl.nt - 1) / (8 * pl.nt));
+  pl.tc = p->dtype == HGA_BF16 && rows >= kQ4TcMinRows && max_list <= hga::kTcMaxList;
+  pl.rows = pl.tc ? hga::kQ4TcRows : p->dtype == HGA_BF16 && rows > 8 ? 16 : 8;
+  pl.n_tiles = (int)((rows + pl.rows - 1) / pl.rows);
   const int64_t ctas = std::max<int64_t>(1, units * pl.n_tiles);
+  if (pl.tc) {
+    // one wave; a split has at least four token tiles
+    pl.n_split = (int)std::max<int64_t>(1, std::min<int64_t>(max_tok / (4 * hga::kTcTok), 148 / ctas));
+    return pl;
+  }
   // a split of at least one step (64 tokens) for every warp
   const int64_t most = std::max<int64_t>(1, (max_tok + 64 * hga::kQ4Warps - 1) / (64 * hga::kQ4Warps));
   pl.n_split = (int)std::min<int64_t>(most, (kQ4TargetCtas + ctas - 1) / ctas);
   return pl;
 }
 
-int64_t q4_work_bytes(const hga_params* p, int64_t parts, int nt) {
-  return parts * 8 * nt * ((int64_t)p->head_dim * 4 + 8);
+int64_t q4_work_bytes(const hga_params* p, int64_t parts, int rows) {
+  return parts * rows * ((int64_t)p->head_dim * 4 + 8);
+}
+
+template <int D, int R, int ENT, typename T, bool ROUTED>
+hga_status launch_q4_join(const hga::Q4AttendArgs& g, int64_t nz, cudaStream_t st) {
+  return launch_pdl(hga::q4_join_kernel<D, R, ENT, T, ROUTED>,
+                    dim3((unsigned)(g.n_tiles * (R > 16 ? R / 16 : 1)), g.a.Hkv, (unsigned)nz),
+                    dim3(128), 0, st, g);
+}
+
+template <int D, bool ROUTED>
+hga_status launch_q4_attend_tc(hga::Q4AttendArgs& g, int64_t nz, cudaStream_t st) {
+  const size_t smem = hga::Q4TcLayout<D>::smem_bytes(ROUTED ? g.a.max_list : 0);
+  hga_status s = allow_smem<hga::q4_attend_tc_kernel<D, ROUTED>, 128>(smem);
+  if (s != HGA_OK) return s;
+  g.shift = hga::kQ4TcShift;
+  dim3 grid((unsigned)(g.n_tiles * g.n_split), g.a.Hkv, (unsigned)nz);
+  s = launch_pdl(hga::q4_attend_tc_kernel<D, ROUTED>, grid, dim3(hga::kQ4TcThreads), smem, st, g);
+  if (s != HGA_OK || g.n_split == 1) return s;
+  return launch_q4_join<D, hga::kQ4TcRows, hga::kQ4TcEnts, __nv_bfloat16, ROUTED>(g, nz, st);
 }
 
 template <int D, int NT, typename T, bool ROUTED>
@@ -1249,22 +1282,25 @@ hga_status launch_q4_attend(hga::Q4AttendArgs& g, int64_t nz, cudaStream_t st) {
   const size_t smem = L::smem_bytes(ROUTED ? g.a.max_list : 0);
   hga_status s = allow_smem<hga::q4_attend_kernel<D, NT, T, ROUTED>>(smem);
   if (s != HGA_OK) return s;
+  g.shift = hga::kQ4PShift;
   dim3 grid((unsigned)(g.n_tiles * g.n_split), g.a.Hkv, (unsigned)nz);
   s = launch_pdl(hga::q4_attend_kernel<D, NT, T, ROUTED>, grid, dim3(32 * hga::kQ4Warps), smem, st,
                  g);
   if (s != HGA_OK || g.n_split == 1) return s;
-  return launch_pdl(hga::q4_join_kernel<D, NT, T, ROUTED>,
-                    dim3((unsigned)g.n_tiles, g.a.Hkv, (unsigned)nz), dim3(128), 0, st, g);
+  return launch_q4_join<D, 8 * NT, 8, T, ROUTED>(g, nz, st);
 }
 
 template <bool ROUTED>
 hga_status q4_dispatch(const hga_params* p, hga::Q4AttendArgs& g, const Q4Plan& pl, int64_t nz,
                        cudaStream_t st) {
   const bool d128 = p->head_dim == 128;
+  if (pl.tc)
+    return d128 ? launch_q4_attend_tc<128, ROUTED>(g, nz, st)
+                : launch_q4_attend_tc<64, ROUTED>(g, nz, st);
   if (p->dtype == HGA_FP32)
     return d128 ? launch_q4_attend<128, 1, float, ROUTED>(g, nz, st)
                 : launch_q4_attend<64, 1, float, ROUTED>(g, nz, st);
-  if (pl.nt == 1)
+  if (pl.rows == 8)
     return d128 ? launch_q4_attend<128, 1, __nv_bfloat16, ROUTED>(g, nz, st)
                 : launch_q4_attend<64, 1, __nv_bfloat16, ROUTED>(g, nz, st);
   return d128 ? launch_q4_attend<128, 2, __nv_bfloat16, ROUTED>(g, nz, st)
@@ -1284,7 +1320,7 @@ void q4_common_args(const hga_params* p, const void* q, void* o, float* lse, con
   g->n_split = pl.n_split;
   g->part_o = static_cast<float*>(work);
   g->part_ml = reinterpret_cast<float2*>(static_cast<char*>(work) +
-                                         pl.parts(units) * 8 * pl.nt * p->head_dim * 4);
+                                         pl.parts(units) * pl.rows * p->head_dim * 4);
 }
 
 }  // namespace
@@ -1424,8 +1460,8 @@ int64_t hga_q4_attend_work(const hga_params* p, int32_t n_seq, int32_t max_q, in
   if (check_params(p) != HGA_OK || n_seq < 0 || max_q < 0 || n_tok < 0 || max_ctx < 0) return -1;
   if (n_seq == 0 || max_q == 0 || n_tok == 0) return 0;
   const int64_t units = (int64_t)n_seq * p->n_kv_heads;
-  const Q4Plan pl = q4_plan(p, units, (int64_t)max_q * (p->n_q_heads / p->n_kv_heads), max_ctx);
-  return q4_work_bytes(p, pl.parts(units), pl.nt);
+  const Q4Plan pl = q4_plan(p, units, (int64_t)max_q * (p->n_q_heads / p->n_kv_heads), max_ctx, 0);
+  return q4_work_bytes(p, pl.parts(units), pl.rows);
 }
 
 hga_status hga_q4_attend(const hga_params* p, const hga_page_pool* pool, int32_t plane,
@@ -1441,8 +1477,8 @@ hga_status hga_q4_attend(const hga_params* p, const hga_page_pool* pool, int32_t
   if (!q || !o || !aligned16(q) || !aligned16(o)) return HGA_ERR_INVALID_ARG;
   if (b->n_seq > 65535 || p->n_kv_heads > 65535 || n_tok > 0x7fffffff) return HGA_ERR_UNSUPPORTED;
   const int64_t units = (int64_t)b->n_seq * p->n_kv_heads;
-  const Q4Plan pl = q4_plan(p, units, (int64_t)b->max_q * (p->n_q_heads / p->n_kv_heads), max_ctx);
-  const int64_t need = q4_work_bytes(p, pl.parts(units), pl.nt);
+  const Q4Plan pl = q4_plan(p, units, (int64_t)b->max_q * (p->n_q_heads / p->n_kv_heads), max_ctx, 0);
+  const int64_t need = q4_work_bytes(p, pl.parts(units), pl.rows);
   if (need > 0 && (!work || !aligned16(work) || work_bytes < need)) return HGA_ERR_INVALID_ARG;
   g.b = hga::Q4BatchArgs{b->rows, b->off, b->n_seq};
   g.max_q = b->max_q;
@@ -1453,8 +1489,8 @@ hga_status hga_q4_attend(const hga_params* p, const hga_page_pool* pool, int32_t
 
 int64_t hga_q4_attend_routed_work(const hga_params* p, int64_t n_q) {
   if (check_params(p) != HGA_OK || n_q < 0) return -1;
-  // units * splits stays below twice the target (q4_plan)
-  return q4_work_bytes(p, 2 * kQ4TargetCtas, 2);
+  // the parts of any q4_plan: below twice the target of 16 rows, or 148 of 256
+  return std::max(q4_work_bytes(p, 2 * kQ4TargetCtas, 16), q4_work_bytes(p, 148, hga::kQ4TcRows));
 }
 
 hga_status hga_q4_attend_routed(const hga_params* p, const hga_page_pool* pool, int32_t plane,
@@ -1493,8 +1529,8 @@ hga_status hga_q4_attend_routed(const hga_params* p, const hga_page_pool* pool, 
   const int64_t block_rows = std::min<int64_t>(p->qblock, q_start + n_q - pos_lo);
   const int64_t units = nz * p->n_kv_heads;
   const Q4Plan pl = q4_plan(p, units, block_rows * (p->n_q_heads / p->n_kv_heads),
-                            std::min<int64_t>(max_list * 8, q_start + n_q));
-  const int64_t need = q4_work_bytes(p, pl.parts(units), pl.nt);
+                            std::min<int64_t>(max_list * 8, q_start + n_q), (int)max_list);
+  const int64_t need = q4_work_bytes(p, pl.parts(units), pl.rows);
   if (need > 0 && (!work || !aligned16(work) || work_bytes < need)) return HGA_ERR_INVALID_ARG;
   q4_common_args(p, q, o, lse, pl, units, work, &g);
   return q4_dispatch<true>(p, g, pl, nz, reinterpret_cast<cudaStream_t>(stream));

@@ -44,6 +44,7 @@ struct Q4AttendArgs {
   int z0;                  // routed: the first block with rows to compute
   int n_split;             // CTAs a unit's tokens are split over
   int n_tiles;             // row tiles a unit can have
+  float shift;             // log2 of the factor that weights and their sums carry
   float* part_o;           // [unit][split][row][D] (n_split > 1)
   float2* part_ml;         // [unit][split][row]  max (log2 units), sum
 };
@@ -539,17 +540,18 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 1) q4_attend_kernel(const Q4Att
   griddep_launch();
 }
 
-// Joins the splits of each unit's rows, in split order.
-template <int D, int NT, typename T, bool ROUTED>
+// Joins the splits of each unit's rows, in split order.  R: rows of a tile, of
+// which a block takes at most 16; ENT: entries of a split's step.
+template <int D, int R, int ENT, typename T, bool ROUTED>
 __global__ void __launch_bounds__(128) q4_join_kernel(const Q4AttendArgs g) {
-  constexpr int R = 8 * NT;
+  constexpr int RB = R < 16 ? R : 16;
   griddep_wait();
-  const int tile = blockIdx.x, h = blockIdx.y;
+  const int tile = blockIdx.x / (R / RB), r_lo = blockIdx.x % (R / RB) * RB, h = blockIdx.y;
   Q4Unit u;
   const int z = blockIdx.z + (ROUTED ? g.z0 : 0);
   if (!q4_unit(g, ROUTED, z, &u)) return;
   const int nrows = u.n * g.a.G, row0 = tile * R;
-  if (row0 >= nrows) return;
+  if (row0 + r_lo >= nrows) return;
   int n_ent;
   if constexpr (ROUTED) {
     const int64_t b0 = g.a.q_start + (int64_t)z * g.a.qblock;
@@ -563,12 +565,12 @@ __global__ void __launch_bounds__(128) q4_join_kernel(const Q4AttendArgs g) {
     const int last_pos = u.pos0 + min(nrows - 1, row0 + R - 1) / g.a.G;
     n_ent = u.row < 0 ? 0 : (last_pos >> 3) + 1;
   }
-  const int steps = (n_ent + 7) / 8;
+  const int steps = (n_ent + ENT - 1) / ENT;
   const int per = max(1, (steps + g.n_split - 1) / g.n_split);
   const int n_s = max(1, (steps + per - 1) / per);     // splits that had tokens
   const int64_t unit = ((int64_t)blockIdx.z * gridDim.y + h) * g.n_tiles + tile;
-  for (int i = threadIdx.x; i < R * (D / 4); i += 128) {
-    const int r = i / (D / 4), c = (i % (D / 4)) * 4;
+  for (int i = threadIdx.x; i < RB * (D / 4); i += 128) {
+    const int r = r_lo + i / (D / 4), c = (i % (D / 4)) * 4;
     if (row0 + r >= nrows) continue;
     const int64_t at0 = unit * g.n_split * R + r;
     float M = -INFINITY, S = 0.f;
@@ -591,7 +593,7 @@ __global__ void __launch_bounds__(128) q4_join_kernel(const Q4AttendArgs g) {
     dst[1] = Elt<T>::from_f32(acc.y * inv);
     dst[2] = Elt<T>::from_f32(acc.z * inv);
     dst[3] = Elt<T>::from_f32(acc.w * inv);
-    if (c == 0 && g.a.lse) g.a.lse[orow] = S > 0.f ? (M + (log2f(S) - kQ4PShift)) * 0.6931471805599453f : -INFINITY;
+    if (c == 0 && g.a.lse) g.a.lse[orow] = S > 0.f ? (M + (log2f(S) - g.shift)) * 0.6931471805599453f : -INFINITY;
   }
   griddep_launch();
 }
