@@ -136,13 +136,12 @@ __device__ __forceinline__ int build_group_list_tc(const AttendArgs& a, int b, i
 // measured 65.5 -> 61.5 us).  It is kept out of line so that its loop runs
 // from registers of its own (inlined into the kernel, whose softmax code sets
 // the register allocation, the loop reloaded spilled values per MMA).
-// QK_BF16: type of Q and K (1 = bf16, 0 = fp16).
-template <int D, int QK_BF16>
-__device__ __forceinline__ void tc_mma_loop(TcBars* bars, uint32_t tmem, uint32_t q_base,
-                                            uint32_t slot_base, int nq, int n_tiles,
-                                            volatile int* abort_flag) {
+template <int D>
+__device__ __noinline__ void tc_mma_issuer(TcBars* bars, uint32_t tmem, uint32_t q_base,
+                                          uint32_t slot_base, int nq, int n_tiles,
+                                          volatile int* abort_flag) {
   using L = TcLayout<D>;
-  constexpr uint32_t kIdS = tc::idesc_f16(kTcRows, kTcTok, QK_BF16, 0);
+  constexpr uint32_t kIdS = tc::idesc_f16(kTcRows, kTcTok, 1, 0);
   constexpr uint32_t kIdPV = tc::idesc_f16(kTcRows, D, 0, 1);
   bool ok = tc::mbar_wait_warp(&bars->q_full, 0, abort_flag);
   tc::fence_after_sync();
@@ -193,13 +192,6 @@ __device__ __forceinline__ void tc_mma_loop(TcBars* bars, uint32_t tmem, uint32_
   const uint64_t t0 = tc::globaltimer_ns();
   while (!tc::mbar_try_wait(&bars->done, 0) && tc::globaltimer_ns() - t0 < tc::kWaitLimitNs) {
   }
-}
-
-template <int D>
-__device__ __noinline__ void tc_mma_issuer(TcBars* bars, uint32_t tmem, uint32_t q_base,
-                                          uint32_t slot_base, int nq, int n_tiles,
-                                          volatile int* abort_flag) {
-  tc_mma_loop<D, 1>(bars, tmem, q_base, slot_base, nq, n_tiles, abort_flag);
 }
 
 template <int D, bool VF16 = false>

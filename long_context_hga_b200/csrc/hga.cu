@@ -488,8 +488,6 @@ hga_status attend_impl(const hga_params* p, const void* q, int64_t q_start, int6
   a.q_early = p->q_ready;
   const int64_t max_list = p->sink / p->group + a.cap_g + p->local / p->group +
                            (p->qblock + p->group - 1) / p->group;
-  if (max_list > 16384) return HGA_ERR_UNSUPPORTED;
-  a.max_list = (int)max_list;
   a.scale_log2 = (float)(1.4426950408889634 / sqrt((double)p->head_dim));
   a.pos_lo = pos_lo;
   if (p->dtype == HGA_BF16 && p->v_f16)
@@ -620,8 +618,6 @@ hga_status hga_attend_backward(const hga_params* p, const void* q, int64_t q_sta
   a.local = p->local;
   const int64_t max_list = p->sink / p->group + a.cap_g + p->local / p->group +
                            (p->qblock + p->group - 1) / p->group;
-  if (max_list > 16384) return HGA_ERR_UNSUPPORTED;
-  a.max_list = (int)max_list;
   w.o = o;
   w.d_o = d_o;
   w.lse = lse;
@@ -1236,9 +1232,9 @@ constexpr int64_t kQ4TargetCtas = 148 * 4;
 constexpr int64_t kQ4TcMinRows = 64;
 
 // rows, max_tok: most query rows and tokens of a unit.
-Q4Plan q4_plan(const hga_params* p, int64_t units, int64_t rows, int64_t max_tok, int max_list) {
+Q4Plan q4_plan(const hga_params* p, int64_t units, int64_t rows, int64_t max_tok) {
   Q4Plan pl;
-  pl.tc = p->dtype == HGA_BF16 && rows >= kQ4TcMinRows && max_list <= hga::kTcMaxList;
+  pl.tc = p->dtype == HGA_BF16 && rows >= kQ4TcMinRows;
   pl.rows = pl.tc ? hga::kQ4TcRows : p->dtype == HGA_BF16 && rows > 8 ? 16 : 8;
   pl.n_tiles = (int)((rows + pl.rows - 1) / pl.rows);
   const int64_t ctas = std::max<int64_t>(1, units * pl.n_tiles);
@@ -1266,20 +1262,20 @@ hga_status launch_q4_join(const hga::Q4AttendArgs& g, int64_t nz, cudaStream_t s
 
 template <int D, bool ROUTED>
 hga_status launch_q4_attend_tc(hga::Q4AttendArgs& g, int64_t nz, cudaStream_t st) {
-  const size_t smem = hga::Q4TcLayout<D>::smem_bytes(ROUTED ? g.a.max_list : 0);
-  hga_status s = allow_smem<hga::q4_attend_tc_kernel<D, ROUTED>, 128>(smem);
+  const size_t smem = hga::Q4TcLayout<D>::kSmem;
+  hga_status s = allow_smem<hga::q4_attend_tc_kernel<D, ROUTED>, hga::kQ4TcLaunchRegs>(smem);
   if (s != HGA_OK) return s;
   g.shift = hga::kQ4TcShift;
   dim3 grid((unsigned)(g.n_tiles * g.n_split), g.a.Hkv, (unsigned)nz);
   s = launch_pdl(hga::q4_attend_tc_kernel<D, ROUTED>, grid, dim3(hga::kQ4TcThreads), smem, st, g);
   if (s != HGA_OK || g.n_split == 1) return s;
-  return launch_q4_join<D, hga::kQ4TcRows, hga::kQ4TcEnts, __nv_bfloat16, ROUTED>(g, nz, st);
+  return launch_q4_join<D, hga::kQ4TcRows, 16, __nv_bfloat16, ROUTED>(g, nz, st);
 }
 
 template <int D, int NT, typename T, bool ROUTED>
 hga_status launch_q4_attend(hga::Q4AttendArgs& g, int64_t nz, cudaStream_t st) {
   using L = hga::Q4Layout<D, NT, ROUTED>;
-  const size_t smem = L::smem_bytes(ROUTED ? g.a.max_list : 0);
+  const size_t smem = L::kSmem;
   hga_status s = allow_smem<hga::q4_attend_kernel<D, NT, T, ROUTED>>(smem);
   if (s != HGA_OK) return s;
   g.shift = hga::kQ4PShift;
@@ -1460,7 +1456,7 @@ int64_t hga_q4_attend_work(const hga_params* p, int32_t n_seq, int32_t max_q, in
   if (check_params(p) != HGA_OK || n_seq < 0 || max_q < 0 || n_tok < 0 || max_ctx < 0) return -1;
   if (n_seq == 0 || max_q == 0 || n_tok == 0) return 0;
   const int64_t units = (int64_t)n_seq * p->n_kv_heads;
-  const Q4Plan pl = q4_plan(p, units, (int64_t)max_q * (p->n_q_heads / p->n_kv_heads), max_ctx, 0);
+  const Q4Plan pl = q4_plan(p, units, (int64_t)max_q * (p->n_q_heads / p->n_kv_heads), max_ctx);
   return q4_work_bytes(p, pl.parts(units), pl.rows);
 }
 
@@ -1477,7 +1473,7 @@ hga_status hga_q4_attend(const hga_params* p, const hga_page_pool* pool, int32_t
   if (!q || !o || !aligned16(q) || !aligned16(o)) return HGA_ERR_INVALID_ARG;
   if (b->n_seq > 65535 || p->n_kv_heads > 65535 || n_tok > 0x7fffffff) return HGA_ERR_UNSUPPORTED;
   const int64_t units = (int64_t)b->n_seq * p->n_kv_heads;
-  const Q4Plan pl = q4_plan(p, units, (int64_t)b->max_q * (p->n_q_heads / p->n_kv_heads), max_ctx, 0);
+  const Q4Plan pl = q4_plan(p, units, (int64_t)b->max_q * (p->n_q_heads / p->n_kv_heads), max_ctx);
   const int64_t need = q4_work_bytes(p, pl.parts(units), pl.rows);
   if (need > 0 && (!work || !aligned16(work) || work_bytes < need)) return HGA_ERR_INVALID_ARG;
   g.b = hga::Q4BatchArgs{b->rows, b->off, b->n_seq};
@@ -1521,15 +1517,13 @@ hga_status hga_q4_attend_routed(const hga_params* p, const hga_page_pool* pool, 
   a.local = p->local;
   a.pos_lo = pos_lo;
   const int64_t max_list = p->sink / p->group + a.cap_g + p->local / p->group + p->qblock / p->group;
-  if (max_list > 16384) return HGA_ERR_UNSUPPORTED;
-  a.max_list = (int)max_list;
   g.row = row;
   g.z0 = (int)((pos_lo - q_start) / p->qblock);
   const int64_t nz = a.n_blocks - g.z0;
   const int64_t block_rows = std::min<int64_t>(p->qblock, q_start + n_q - pos_lo);
   const int64_t units = nz * p->n_kv_heads;
   const Q4Plan pl = q4_plan(p, units, block_rows * (p->n_q_heads / p->n_kv_heads),
-                            std::min<int64_t>(max_list * 8, q_start + n_q), (int)max_list);
+                            std::min<int64_t>(max_list * 8, q_start + n_q));
   const int64_t need = q4_work_bytes(p, pl.parts(units), pl.rows);
   if (need > 0 && (!work || !aligned16(work) || work_bytes < need)) return HGA_ERR_INVALID_ARG;
   q4_common_args(p, q, o, lse, pl, units, work, &g);

@@ -51,16 +51,15 @@ struct Q4AttendArgs {
 
 template <int D, int NT, bool ROUTED>
 struct Q4Layout {
-  // the routed form keeps its group list beside the rings
-  static constexpr int kStages = ROUTED ? 2 : 3;
+  static constexpr int kStages = 3;
   static constexpr int kRec = q4_record_bytes(D);
   static constexpr int kStage = 8 * kRec;
   static constexpr int kRingOff = 0;
   static constexpr int kRing = kQ4Warps * kStages * kStage;
   static constexpr int kJoin = kQ4Warps * 8 * NT * (D + 2) * 4;     // reuses the ring
   static constexpr int kBarOff = kRing > kJoin ? kRing : kJoin;
-  static constexpr int kListOff = kBarOff + kQ4Warps * kStages * 16;
-  static constexpr size_t smem_bytes(int max_list) { return (size_t)kListOff + (size_t)max_list * 4; }
+  static constexpr int kEntOff = kBarOff + kQ4Warps * kStages * 8;   // [warp][stage][8] entries
+  static constexpr size_t kSmem = kEntOff + kQ4Warps * kStages * 32;
 };
 
 __device__ __forceinline__ void q4_mma(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
@@ -139,6 +138,95 @@ __device__ __forceinline__ bool q4_unit(const Q4AttendArgs& g, bool routed, int 
   return true;
 }
 
+// The records that a unit attends, in order: dense, those of its tokens; routed,
+// the sink, routed, local-window and diagonal groups of hga_attend.
+struct Q4List {
+  int n;                   // entries
+  int n_whole;             // entries that every row attends whole
+  int n_s, n_r, loc0, n_l, d0;
+  int lo, hi;              // routed groups lie in [lo, hi)
+  const int32_t* routed;
+};
+
+// dense: first_pos and last_pos are the positions of the first and last row.
+template <bool ROUTED>
+__device__ __forceinline__ Q4List q4_list(const Q4AttendArgs& g, const Q4Unit& u, int z, int h,
+                                          int first_pos, int last_pos) {
+  Q4List x{};
+  if constexpr (ROUTED) {
+    const int64_t b0 = g.a.q_start + (int64_t)z * g.a.qblock;
+    const int64_t sink_end = min((int64_t)g.a.sink, b0);
+    const int64_t loc_lo = max(sink_end, b0 - g.a.local);
+    x.n_s = (int)(sink_end / 8);
+    x.n_r = g.a.group_cnt[(int64_t)h * g.a.n_blocks + z];
+    if (x.n_r < 0 || x.n_r > g.a.cap_g) {
+      report(HGA_ERR_DEVICE_CHECK);
+      x.n_r = 0;
+    }
+    x.loc0 = (int)(loc_lo / 8);
+    x.n_l = (int)((b0 - loc_lo) / 8);
+    x.d0 = (int)(b0 / 8);
+    x.lo = g.a.sink / 8;
+    x.hi = (int)((b0 - g.a.local) / 8);
+    x.routed = g.a.group_idx + ((int64_t)h * g.a.n_blocks + z) * g.a.cap_g;
+    x.n_whole = x.n_s + x.n_r + x.n_l;
+    x.n = x.n_whole + (last_pos + 1 - (int)b0 + 7) / 8;
+  } else if (u.row >= 0) {
+    x.n = (last_pos >> 3) + 1;
+    x.n_whole = (first_pos + 1) >> 3;
+  }
+  return x;
+}
+
+// Entry i (a record of the sequence), -1 where there is none: past the end, or
+// a routed group that is not legal (reported).
+template <bool ROUTED>
+__device__ __forceinline__ int q4_entry(const Q4List& x, int i) {
+  if (i < 0 || i >= x.n) return -1;
+  if constexpr (!ROUTED) return i;
+  if (i < x.n_s) return i;
+  int r = i - x.n_s;
+  if (r < x.n_r) {
+    const int e = x.routed[r], before = r > 0 ? x.routed[r - 1] : -1;
+    if (e >= x.lo && e < x.hi && e > before) return e;
+    report(HGA_ERR_DEVICE_CHECK);
+    return -1;
+  }
+  r -= x.n_r;
+  return r < x.n_l ? x.loc0 + r : x.d0 + r - x.n_l;
+}
+
+// Byte offset of a record from the plane's first page, -1 (reported) where the
+// page table names none.
+__device__ __forceinline__ int64_t q4_where(const Q4Cache& c, const int32_t* pages, int h, int ent,
+                                            int rec_bytes) {
+  const int col = ent / c.page_recs, in = ent - col * c.page_recs;
+  const int pg = col < c.row_pages ? pages[col] : -1;
+  if (pg < 0 || pg >= c.n_pages) {
+    report(HGA_ERR_DEVICE_CHECK);
+    return -1;
+  }
+  return pg * c.page_bytes + ((int64_t)h * c.page_recs + in) * rec_bytes;
+}
+
+// Fetches up to 8 records (lane e < 8 holds record e's offset, -1 for none) to
+// dst + e * rec.  Records that follow one another in memory come in one copy:
+// a copy's cost is in its issue (one of 576 or 1152 bytes per record kept the
+// expanding warps of q4_attend_tc.cuh waiting for 60% of the time).  Arms bar.
+__device__ __forceinline__ void q4_fetch8(char* dst, const char* base, int64_t at, int rec,
+                                          uint64_t* bar, int lane) {
+  const int64_t before = __shfl_up_sync(0xffffffffu, at, 1);
+  const unsigned live = __ballot_sync(0xffffffffu, at >= 0);
+  const bool first = at >= 0 && (lane == 0 || before < 0 || at != before + rec);
+  const unsigned stops = __ballot_sync(0xffffffffu, first) | ~live;
+  if (lane == 0) tc::mbar_arrive_expect_tx(bar, __popc(live) * rec);
+  __syncwarp();
+  if (first) {
+    const unsigned after = stops & (0xfffffffeu << lane);
+    bulk_load(dst + lane * rec, base + at, (__ffs(after) - 1 - lane) * rec, bar);
+  }
+}
+
 // Steps of 64 tokens (or 8 list entries) of one split.
 __device__ __forceinline__ void q4_split_range(int steps, int n_split, int split, int* lo, int* hi) {
   const int per = (steps + n_split - 1) / n_split;
@@ -154,14 +242,14 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 1) q4_attend_kernel(const Q4Att
   constexpr int KS = D / 16;                    // k-steps of S, m-tiles of O
   constexpr int R = 8 * NT;
   extern __shared__ __align__(128) char smem[];
-  int* list = reinterpret_cast<int*>(smem + L::kListOff);
-  __shared__ int s_abort, s_inv;
+  __shared__ int s_abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gr = lane >> 2, t = lane & 3;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff) + warp * kQ4Stages;
   char* ring = smem + L::kRingOff + warp * kQ4Stages * L::kStage;
+  int* ents = reinterpret_cast<int*>(smem + L::kEntOff) + warp * kQ4Stages * 8;
 
-  if (tid == 0) s_abort = s_inv = 0;
+  if (tid == 0) s_abort = 0;
   if (lane == 0) {
     for (int s = 0; s < kQ4Stages; ++s) tc::mbar_init(&bars[s], 1);
     tc::fence_mbar_init();
@@ -177,18 +265,8 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 1) q4_attend_kernel(const Q4Att
   if (row0 >= nrows) return;
   const int last_pos = u.pos0 + min(nrows - 1, row0 + R - 1) / g.a.G;
   const int first_pos = u.pos0 + row0 / g.a.G;
-  int n_ent, n_nondiag = 0;                     // 8-token entries
-  if constexpr (ROUTED) {
-    bool inv = false;
-    __syncthreads();
-    const int64_t b0 = g.a.q_start + (int64_t)z * g.a.qblock;
-    n_ent = max(0, build_group_list(g.a, z, h, b0, u.ctx, list, &n_nondiag, &inv));
-    if (inv) s_inv = 1;
-  } else {
-    n_ent = u.row < 0 ? 0 : (last_pos >> 3) + 1;
-  }
-  __syncthreads();
-  const bool any_inv = ROUTED && s_inv;
+  const Q4List list = q4_list<ROUTED>(g, u, z, h, first_pos, last_pos);
+  const int n_ent = list.n;
   const int steps = (n_ent + 7) / 8;
   int lo, hi;
   q4_split_range(steps, g.n_split, split, &lo, &hi);
@@ -200,21 +278,12 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 1) q4_attend_kernel(const Q4Att
   unsigned got[kQ4Stages];                      // records that were fetched, per stage
   int issued = 0;
   auto fetch = [&](int i, int s) -> unsigned {
-    const int e = (lo + warp + i * kQ4Warps) * 8 + lane;
-    int ent = -1;
-    if (lane < 8 && e < n_ent) ent = ROUTED ? list[e] : e;
-    const char* src = nullptr;
-    if (ent >= 0) {
-      const int col = ent / g.c.page_recs, in = ent - col * g.c.page_recs;
-      const int pg = col < g.c.row_pages ? pages[col] : -1;
-      if (pg < 0 || pg >= g.c.n_pages) report(HGA_ERR_DEVICE_CHECK);
-      else src = g.c.base + pg * g.c.page_bytes + ((int64_t)h * g.c.page_recs + in) * L::kRec;
-    }
-    const unsigned m = __ballot_sync(0xffffffffu, src != nullptr);
+    int ent = lane < 8 ? q4_entry<ROUTED>(list, (lo + warp + i * kQ4Warps) * 8 + lane) : -1;
+    const int64_t at = ent >= 0 ? q4_where(g.c, pages, h, ent, L::kRec) : -1;
+    if (lane < 8) ents[s * 8 + lane] = at >= 0 ? ent : -1;
+    const unsigned m = __ballot_sync(0xffffffffu, at >= 0);
     ++issued;
-    if (lane == 0) tc::mbar_arrive_expect_tx(&bars[s], __popc(m) * L::kRec);
-    __syncwarp();
-    if (src) bulk_load(ring + s * L::kStage + lane * L::kRec, src, L::kRec, &bars[s]);
+    q4_fetch8(ring + s * L::kStage, g.c.base, at, L::kRec, &bars[s], lane);
     return m;
   };
 #pragma unroll
@@ -287,8 +356,8 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 1) q4_attend_kernel(const Q4Att
 #pragma unroll
     for (int x = 1; x < kQ4Stages; ++x) if (s == x) have = got[x];
     const int e0 = (lo + warp + i * kQ4Warps) * 8;
-    const bool edge = have != 0xffu || any_inv ||
-                      (ROUTED ? e0 + 8 > n_nondiag : e0 * 8 + 63 > first_pos);
+    const bool edge = have != 0xffu || e0 + 8 > list.n_whole;
+    const int* ent_of = ents + s * 8;
     // ---- scores
     float sv[4][NT][4];
 #pragma unroll
@@ -345,8 +414,8 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 1) q4_attend_kernel(const Q4Att
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
           const int rec = 2 * mt + y;
-          const int ent = ROUTED ? (e0 + rec < n_ent ? list[e0 + rec] : -1) : e0 + rec;
-          const bool there = (have >> rec) & 1;
+          const int ent = ent_of[rec];
+          const bool there = ent >= 0;
           const int tok = ent * 8 + tok_k;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
@@ -432,8 +501,8 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 1) q4_attend_kernel(const Q4Att
         if (edge) {
           // tokens that no row attends may hold anything: 0 * scale 0
           const int r = 2 * mt + (y >> 1);
-          const int ent = ROUTED ? (e0 + r < n_ent ? list[e0 + r] : -1) : e0 + r;
-          if (!((have >> r) & 1) || ent * 8 + tk > last_pos) b4[y] = 0;
+          const int ent = ent_of[r];
+          if (ent < 0 || ent * 8 + tk > last_pos) b4[y] = 0;
         }
       }
       sab = b4[0] << 7 | b4[1] << 23;
@@ -552,19 +621,8 @@ __global__ void __launch_bounds__(128) q4_join_kernel(const Q4AttendArgs g) {
   if (!q4_unit(g, ROUTED, z, &u)) return;
   const int nrows = u.n * g.a.G, row0 = tile * R;
   if (row0 + r_lo >= nrows) return;
-  int n_ent;
-  if constexpr (ROUTED) {
-    const int64_t b0 = g.a.q_start + (int64_t)z * g.a.qblock;
-    const int64_t sink_end = min((int64_t)g.a.sink, b0);
-    const int64_t loc_lo = max(sink_end, b0 - g.a.local);
-    int n_r = g.a.group_cnt[(int64_t)h * g.a.n_blocks + z];
-    if (n_r < 0 || n_r > g.a.cap_g) n_r = 0;
-    n_ent = (int)(sink_end / 8 + n_r + (b0 - loc_lo) / 8 + (min(b0 + g.a.qblock, (int64_t)u.ctx) - b0 + 7) / 8);
-    if (n_ent > g.a.max_list) n_ent = 0;
-  } else {
-    const int last_pos = u.pos0 + min(nrows - 1, row0 + R - 1) / g.a.G;
-    n_ent = u.row < 0 ? 0 : (last_pos >> 3) + 1;
-  }
+  const int n_ent = q4_list<ROUTED>(g, u, z, h, u.pos0 + row0 / g.a.G,
+                                    u.pos0 + min(nrows - 1, row0 + R - 1) / g.a.G).n;
   const int steps = (n_ent + ENT - 1) / ENT;
   const int per = max(1, (steps + g.n_split - 1) / g.n_split);
   const int n_s = max(1, (steps + per - 1) / per);     // splits that had tokens

@@ -182,8 +182,6 @@ def test_q4_refuses(hga):
     for bad in (dict(work=None), dict(work=FAKE + 8), dict(size=16)):
         assert routed(p=wide, q0=2048, lo=2048, cap=4096, pool=_pool(hga, row_pages=64), **bad) == 1
     assert routed(lo=128) == 0                               # no row is asked for
-    big = P(8, 2, 128, top_chunks=0, top_groups=0).c()
-    assert routed(p=big, cap=1 << 18, pool=_pool(hga, row_pages=1 << 12)) == 2
     assert L.hga_q4_page_bytes(B(ok), 64) == 2 * 8 * 1152
     assert L.hga_q4_page_bytes(B(P(8, 2, 64).c()), 8) == 2 * 576
     assert L.hga_q4_page_bytes(B(ok), 60) == -1 and L.hga_q4_page_bytes(None, 64) == -1
