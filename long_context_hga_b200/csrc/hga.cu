@@ -1221,31 +1221,42 @@ unsigned q4_io_grid(const hga::Q4IoArgs& a) {
 // ---------------------------------------------------------------- 4-bit attention
 
 // How a call is cut: the kernel, rows per tile, tiles of a unit, CTAs per unit
-// and tile.
+// and tile, or CTAs that all sequences share (slots).
 struct Q4Plan {
   bool tc = false;
-  int rows = 8, n_tiles = 1, n_split = 1;
-  int64_t parts(int64_t units) const { return n_split > 1 ? units * n_tiles * n_split : 0; }
+  int rows = 8, n_tiles = 1, n_split = 1, slots = 0;
+  int64_t parts(int64_t units, int64_t n_kv_heads) const {
+    return slots ? n_kv_heads * slots * n_tiles : n_split > 1 ? units * n_tiles * n_split : 0;
+  }
 };
 
-constexpr int64_t kQ4TargetCtas = 148 * 4;
 constexpr int64_t kQ4TcMinRows = 64;
 
-// rows, max_tok: most query rows and tokens of a unit.
-Q4Plan q4_plan(const hga_params* p, int64_t units, int64_t rows, int64_t max_tok) {
+// rows, max_tok: most query rows and tokens of a unit; n_seq: sequences of a
+// dense call, 0 for a routed one.
+Q4Plan q4_plan(const hga_params* p, int64_t units, int64_t rows, int64_t max_tok, int64_t n_seq) {
   Q4Plan pl;
   pl.tc = p->dtype == HGA_BF16 && rows >= kQ4TcMinRows;
   pl.rows = pl.tc ? hga::kQ4TcRows : p->dtype == HGA_BF16 && rows > 8 ? 16 : 8;
   pl.n_tiles = (int)((rows + pl.rows - 1) / pl.rows);
   const int64_t ctas = std::max<int64_t>(1, units * pl.n_tiles);
   if (pl.tc) {
-    // one wave; a split has at least four token tiles
+    // one wave; a split has at least four steps
     pl.n_split = (int)std::max<int64_t>(1, std::min<int64_t>(max_tok / (4 * hga::kTcTok), 148 / ctas));
     return pl;
   }
-  // a split of at least one step (64 tokens) for every warp
-  const int64_t most = std::max<int64_t>(1, (max_tok + 64 * hga::kQ4Warps - 1) / (64 * hga::kQ4Warps));
-  pl.n_split = (int)std::min<int64_t>(most, (kQ4TargetCtas + ctas - 1) / ctas);
+  // one wave of the CTAs that an SM holds at a time (8 requests at up to 64K, 32
+  // heads on 4: one wave 79 us, two 91, three 105); a split has at least one
+  // step for every warp
+  const int64_t wave = 148 * (p->dtype == HGA_BF16 && pl.rows == 8 ? 3 : 2);
+  const int64_t most = (max_tok + 64 * hga::kQ4Warps - 1) / (64 * hga::kQ4Warps);
+  if (most <= 1) return pl;
+  if (n_seq > 0) {
+    const int64_t slots = std::min(wave / ((int64_t)p->n_kv_heads * pl.n_tiles), n_seq * most);
+    if (slots > n_seq) pl.slots = (int)slots;
+  } else {
+    pl.n_split = (int)std::max<int64_t>(1, std::min(most, wave / ctas));
+  }
   return pl;
 }
 
@@ -1279,10 +1290,11 @@ hga_status launch_q4_attend(hga::Q4AttendArgs& g, int64_t nz, cudaStream_t st) {
   hga_status s = allow_smem<hga::q4_attend_kernel<D, NT, T, ROUTED>>(smem);
   if (s != HGA_OK) return s;
   g.shift = hga::kQ4PShift;
-  dim3 grid((unsigned)(g.n_tiles * g.n_split), g.a.Hkv, (unsigned)nz);
+  dim3 grid((unsigned)(g.n_tiles * (g.slots ? g.slots : g.n_split)), g.a.Hkv,
+            (unsigned)(g.slots ? 1 : nz));
   s = launch_pdl(hga::q4_attend_kernel<D, NT, T, ROUTED>, grid, dim3(32 * hga::kQ4Warps), smem, st,
                  g);
-  if (s != HGA_OK || g.n_split == 1) return s;
+  if (s != HGA_OK || (g.n_split == 1 && !g.slots)) return s;
   return launch_q4_join<D, 8 * NT, 8, T, ROUTED>(g, nz, st);
 }
 
@@ -1314,9 +1326,10 @@ void q4_common_args(const hga_params* p, const void* q, void* o, float* lse, con
   g->a.scale_log2 = (float)(1.4426950408889634 / sqrt((double)p->head_dim));
   g->n_tiles = pl.n_tiles;
   g->n_split = pl.n_split;
+  g->slots = pl.slots;
   g->part_o = static_cast<float*>(work);
   g->part_ml = reinterpret_cast<float2*>(static_cast<char*>(work) +
-                                         pl.parts(units) * pl.rows * p->head_dim * 4);
+                                         pl.parts(units, p->n_kv_heads) * pl.rows * p->head_dim * 4);
 }
 
 }  // namespace
@@ -1456,8 +1469,8 @@ int64_t hga_q4_attend_work(const hga_params* p, int32_t n_seq, int32_t max_q, in
   if (check_params(p) != HGA_OK || n_seq < 0 || max_q < 0 || n_tok < 0 || max_ctx < 0) return -1;
   if (n_seq == 0 || max_q == 0 || n_tok == 0) return 0;
   const int64_t units = (int64_t)n_seq * p->n_kv_heads;
-  const Q4Plan pl = q4_plan(p, units, (int64_t)max_q * (p->n_q_heads / p->n_kv_heads), max_ctx);
-  return q4_work_bytes(p, pl.parts(units), pl.rows);
+  const Q4Plan pl = q4_plan(p, units, (int64_t)max_q * (p->n_q_heads / p->n_kv_heads), max_ctx, n_seq);
+  return q4_work_bytes(p, pl.parts(units, p->n_kv_heads), pl.rows);
 }
 
 hga_status hga_q4_attend(const hga_params* p, const hga_page_pool* pool, int32_t plane,
@@ -1473,8 +1486,8 @@ hga_status hga_q4_attend(const hga_params* p, const hga_page_pool* pool, int32_t
   if (!q || !o || !aligned16(q) || !aligned16(o)) return HGA_ERR_INVALID_ARG;
   if (b->n_seq > 65535 || p->n_kv_heads > 65535 || n_tok > 0x7fffffff) return HGA_ERR_UNSUPPORTED;
   const int64_t units = (int64_t)b->n_seq * p->n_kv_heads;
-  const Q4Plan pl = q4_plan(p, units, (int64_t)b->max_q * (p->n_q_heads / p->n_kv_heads), max_ctx);
-  const int64_t need = q4_work_bytes(p, pl.parts(units), pl.rows);
+  const Q4Plan pl = q4_plan(p, units, (int64_t)b->max_q * (p->n_q_heads / p->n_kv_heads), max_ctx, b->n_seq);
+  const int64_t need = q4_work_bytes(p, pl.parts(units, p->n_kv_heads), pl.rows);
   if (need > 0 && (!work || !aligned16(work) || work_bytes < need)) return HGA_ERR_INVALID_ARG;
   g.b = hga::Q4BatchArgs{b->rows, b->off, b->n_seq};
   g.max_q = b->max_q;
@@ -1485,8 +1498,8 @@ hga_status hga_q4_attend(const hga_params* p, const hga_page_pool* pool, int32_t
 
 int64_t hga_q4_attend_routed_work(const hga_params* p, int64_t n_q) {
   if (check_params(p) != HGA_OK || n_q < 0) return -1;
-  // the parts of any q4_plan: below twice the target of 16 rows, or 148 of 256
-  return std::max(q4_work_bytes(p, 2 * kQ4TargetCtas, 16), q4_work_bytes(p, 148, hga::kQ4TcRows));
+  // the parts of any q4_plan: at most a wave of CTAs
+  return std::max(q4_work_bytes(p, 148 * 3, 16), q4_work_bytes(p, 148, hga::kQ4TcRows));
 }
 
 hga_status hga_q4_attend_routed(const hga_params* p, const hga_page_pool* pool, int32_t plane,
@@ -1523,8 +1536,8 @@ hga_status hga_q4_attend_routed(const hga_params* p, const hga_page_pool* pool, 
   const int64_t block_rows = std::min<int64_t>(p->qblock, q_start + n_q - pos_lo);
   const int64_t units = nz * p->n_kv_heads;
   const Q4Plan pl = q4_plan(p, units, block_rows * (p->n_q_heads / p->n_kv_heads),
-                            std::min<int64_t>(max_list * 8, q_start + n_q));
-  const int64_t need = q4_work_bytes(p, pl.parts(units), pl.rows);
+                            std::min<int64_t>(max_list * 8, q_start + n_q), 0);
+  const int64_t need = q4_work_bytes(p, pl.parts(units, p->n_kv_heads), pl.rows);
   if (need > 0 && (!work || !aligned16(work) || work_bytes < need)) return HGA_ERR_INVALID_ARG;
   q4_common_args(p, q, o, lse, pl, units, work, &g);
   return q4_dispatch<true>(p, g, pl, nz, reinterpret_cast<cudaStream_t>(stream));

@@ -28,11 +28,12 @@
 
 namespace hga {
 
-constexpr int kQ4Warps = 8;
+constexpr int kQ4Warps = 4;
 constexpr int kQ4StepTok = 64;            // tokens a warp takes at a time
-// Weights are held as 2^15 times exp(score - max), so that fp16 keeps 11 bits
-// of those down to 2^-29 of the largest one (its subnormals start at 2^-14).
-constexpr float kQ4PShift = 15.f;
+// Weights are held as 2^11 times exp(score - m), m a maximum that is only moved
+// when a score passes it by more than 2^4: at most 2^15 in fp16, with 11 bits
+// down to 2^-25 of the largest one (fp16's subnormals start at 2^-14).
+constexpr float kQ4PShift = 11.f, kQ4Grow = 4.f;
 
 struct Q4AttendArgs {
   Q4Cache c;
@@ -43,15 +44,17 @@ struct Q4AttendArgs {
   int row;                 // routed: the sequence's table row
   int z0;                  // routed: the first block with rows to compute
   int n_split;             // CTAs a unit's tokens are split over
+  int slots;               // dense, few rows: CTAs per KV head and tile that all the sequences'
+                           // tokens are dealt out to (see q4_deal), 0 = one per sequence
   int n_tiles;             // row tiles a unit can have
   float shift;             // log2 of the factor that weights and their sums carry
-  float* part_o;           // [unit][split][row][D] (n_split > 1)
+  float* part_o;           // [unit][split][row][D] (n_split > 1) or [KV head][slot][tile][row][D]
   float2* part_ml;         // [unit][split][row]  max (log2 units), sum
 };
 
 template <int D, int NT, bool ROUTED>
 struct Q4Layout {
-  static constexpr int kStages = 3;
+  static constexpr int kStages = 2;
   static constexpr int kRec = q4_record_bytes(D);
   static constexpr int kStage = 8 * kRec;
   static constexpr int kRingOff = 0;
@@ -227,6 +230,52 @@ __device__ __forceinline__ void q4_fetch8(char* dst, const char* base, int64_t a
   }
 }
 
+// The batch's tokens dealt out to `slots` CTAs (more than sequences): every
+// sequence gets as many as its length needs at `per` steps each, at least one,
+// with `per` the least that makes them suffice: sum ceil(steps / per) <= n_seq +
+// total / per.  Only the device knows the lengths, and a split into as many
+// parts for every sequence leaves the longest ones' CTAs running last.
+__device__ __forceinline__ int q4_seq_steps(const Q4AttendArgs& g, int z) {
+  const int r = g.b.rows[z];
+  if (r < 0 || r >= g.c.n_rows) return 0;
+  const int ctx = g.c.len[r];
+  return ctx <= 0 || ctx > (int64_t)g.c.row_pages * g.c.page_tokens ? 0 : (ctx + 63) / 64;
+}
+__device__ __forceinline__ int q4_deal(const Q4AttendArgs& g, int lane) {
+  int64_t total = 0;
+  for (int z = lane; z < g.b.n_seq; z += 32) total += q4_seq_steps(g, z);
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) total += __shfl_xor_sync(0xffffffffu, total, x);
+  const int64_t spare = g.slots - g.b.n_seq;
+  return (int)max((int64_t)kQ4Warps, (total + spare - 1) / spare);
+}
+// Which sequence and part of it a slot has (find = -1), or the first slot of
+// sequence `find`.  False: the slot has none.
+__device__ __forceinline__ bool q4_dealt(const Q4AttendArgs& g, int per, int lane, int find, int* slot,
+                                         int* z) {
+  int base = 0;
+  for (int z0 = 0; z0 < g.b.n_seq; z0 += 32) {
+    const int n = z0 + lane < g.b.n_seq ? max(1, (q4_seq_steps(g, z0 + lane) + per - 1) / per) : 0;
+    int incl = n;
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, x);
+      if (lane >= x) incl += y;
+    }
+    const int all = __shfl_sync(0xffffffffu, incl, 31);
+    if (find >= 0 ? find < z0 + 32 : *slot < base + all) {
+      const unsigned past = __ballot_sync(0xffffffffu, *slot < base + incl);
+      const int at = find >= 0 ? find - z0 : __ffs(past) - 1;
+      const int first = base + __shfl_sync(0xffffffffu, incl - n, at);
+      *z = z0 + at;
+      *slot = find >= 0 ? first : *slot - first;
+      return true;
+    }
+    base += all;
+  }
+  return false;
+}
+
 // Steps of 64 tokens (or 8 list entries) of one split.
 __device__ __forceinline__ void q4_split_range(int steps, int n_split, int split, int* lo, int* hi) {
   const int per = (steps + n_split - 1) / n_split;
@@ -234,8 +283,14 @@ __device__ __forceinline__ void q4_split_range(int steps, int n_split, int split
   *hi = min(steps, *lo + per);
 }
 
+// CTAs of an SM: what the registers allow (the rings leave room for three).
+// The loads, conversions and products of a step are one chain in a warp, so
+// the more warps the better.
+template <int NT, typename T>
+constexpr int q4_ctas() { return NT == 1 && sizeof(T) == 2 ? 3 : 2; }
+
 template <int D, int NT, typename T, bool ROUTED>
-__global__ void __launch_bounds__(32 * kQ4Warps, 1) q4_attend_kernel(const Q4AttendArgs g) {
+__global__ void __launch_bounds__(32 * kQ4Warps, (q4_ctas<NT, T>())) q4_attend_kernel(const Q4AttendArgs g) {
   using L = Q4Layout<D, NT, ROUTED>;
   constexpr int kQ4Stages = L::kStages;
   constexpr bool kSplitFp = sizeof(T) == 4;     // fp32: q and P as sums of two fp16 values
@@ -255,10 +310,18 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 1) q4_attend_kernel(const Q4Att
     tc::fence_mbar_init();
   }
   griddep_wait();
-  const int tile = blockIdx.x / g.n_split, split = blockIdx.x % g.n_split;
   const int h = blockIdx.y;
+  const int n_x = !ROUTED && g.slots ? g.slots : g.n_split;
+  const int tile = blockIdx.x / n_x;
+  int split = blockIdx.x % n_x;
+  int z = blockIdx.z + (ROUTED ? g.z0 : 0), per = 0;
+  int64_t part = (((int64_t)blockIdx.z * gridDim.y + h) * g.n_tiles + tile) * n_x + split;
+  if (!ROUTED && g.slots) {
+    part = ((int64_t)h * n_x + split) * g.n_tiles + tile;
+    per = q4_deal(g, lane);
+    if (!q4_dealt(g, per, lane, -1, &split, &z)) return;
+  }
   Q4Unit u;
-  const int z = blockIdx.z + (ROUTED ? g.z0 : 0);
   if (!q4_unit(g, ROUTED, z, &u)) return;
   const int nrows = u.n * g.a.G;
   const int row0 = tile * R;
@@ -269,8 +332,14 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 1) q4_attend_kernel(const Q4Att
   const int n_ent = list.n;
   const int steps = (n_ent + 7) / 8;
   int lo, hi;
-  q4_split_range(steps, g.n_split, split, &lo, &hi);
+  if (per) {
+    lo = min(steps, split * per);
+    hi = min(steps, lo + per);
+  } else {
+    q4_split_range(steps, g.n_split, split, &lo, &hi);
+  }
   if (lo >= hi && split > 0) return;            // the join reads only splits with tokens
+  const bool whole = per ? steps <= per : g.n_split == 1;   // nothing to join
 
   // ---- the warp's loads: lane l < 8 fetches record l of a step
   const int32_t* pages = g.c.table + (int64_t)max(u.row, 0) * g.c.row_pages;
@@ -427,21 +496,43 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 1) q4_attend_kernel(const Q4Att
     // ---- softmax over the step's 64 tokens.  m is a score, not yet scaled: the
     // difference to it is taken first, so that it stays <= 0 however large
     // scores are
-    float corr[NT][2];
     uint32_t ph[4][NT][2], pl[kSplitFp ? 4 : 1][NT][2];
+    float top[NT][2];
+    bool grow = false;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         float mx = -INFINITY;
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt) mx = fmaxf(mx, fmaxf(sv[mt][nt][x], sv[mt][nt][2 + x]));
+        top[nt][x] = mx;
+        grow |= m[nt][x] == -INFINITY ? mx > -INFINITY : (mx - m[nt][x]) * sc[nt][x] > kQ4Grow;
+      }
+    if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-        for (int q = 4; q < 32; q <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, q));
-        const float mn = fmaxf(m[nt][x], mx);
-        const float use = mn == -INFINITY ? 0.f : mn;
-        corr[nt][x] = tc::ex2((m[nt][x] - use) * sc[nt][x]);
-        m[nt][x] = mn;
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          float mx = top[nt][x];
+#pragma unroll
+          for (int q = 4; q < 32; q <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, q));
+          const float mn = fmaxf(m[nt][x], mx);
+          const float corr = mn == -INFINITY ? 1.f : tc::ex2((m[nt][x] - mn) * sc[nt][x]);
+          m[nt][x] = mn;
+          l[nt][x] *= corr;
+#pragma unroll
+          for (int j = 0; j < KS; ++j) {
+            o[j][nt][x] *= corr;
+            o[j][nt][2 + x] *= corr;
+          }
+        }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const float use = m[nt][x] == -INFINITY ? 0.f : m[nt][x];
         float sum = 0.f;
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt)
@@ -451,7 +542,7 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 1) q4_attend_kernel(const Q4Att
             p = tc::ex2(fmaf(p - use, sc[nt][x], kQ4PShift));
             sum += p;
           }
-        l[nt][x] = l[nt][x] * corr[nt][x] + sum;
+        l[nt][x] += sum;
       }
 #pragma unroll
       for (int mt = 0; mt < 4; ++mt)
@@ -464,18 +555,6 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 1) q4_attend_kernel(const Q4Att
           } else {
             ph[mt][nt][y] = transpose8(tc::pack_half2(sv[mt][nt][2 * y], sv[mt][nt][2 * y + 1]));
           }
-        }
-    }
-    bool move = false;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) move |= corr[nt][0] != 1.f || corr[nt][1] != 1.f;
-    if (__any_sync(0xffffffffu, move)) {
-#pragma unroll
-      for (int j = 0; j < KS; ++j)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          o[j][nt][0] *= corr[nt][0]; o[j][nt][1] *= corr[nt][1];
-          o[j][nt][2] *= corr[nt][0]; o[j][nt][3] *= corr[nt][1];
         }
     }
     // ---- O^T += V^T P^T
@@ -590,9 +669,8 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 1) q4_attend_kernel(const Q4Att
       acc.x += v.x * f; acc.y += v.y * f; acc.z += v.z * f; acc.w += v.w * f;
     }
     const int pr = row0 + r;
-    if (g.n_split > 1) {
-      const int64_t unit = ((int64_t)blockIdx.z * gridDim.y + h) * g.n_tiles + tile;
-      const int64_t at = (unit * g.n_split + split) * R + r;
+    if (!whole) {
+      const int64_t at = part * R + r;
       *reinterpret_cast<float4*>(g.part_o + at * D + c) = acc;
       if (c == 0) g.part_ml[at] = make_float2(M, S);
       continue;
@@ -624,19 +702,27 @@ __global__ void __launch_bounds__(128) q4_join_kernel(const Q4AttendArgs g) {
   const int n_ent = q4_list<ROUTED>(g, u, z, h, u.pos0 + row0 / g.a.G,
                                     u.pos0 + min(nrows - 1, row0 + R - 1) / g.a.G).n;
   const int steps = (n_ent + ENT - 1) / ENT;
-  const int per = max(1, (steps + g.n_split - 1) / g.n_split);
+  int per = max(1, (steps + g.n_split - 1) / g.n_split);
+  int64_t part0 = (((int64_t)blockIdx.z * gridDim.y + h) * g.n_tiles + tile) * g.n_split, stride = R;
+  if (!ROUTED && g.slots) {
+    int slot = 0, zz;
+    per = q4_deal(g, threadIdx.x & 31);
+    if (steps <= per) return;                          // already whole
+    q4_dealt(g, per, threadIdx.x & 31, z, &slot, &zz);
+    part0 = ((int64_t)h * g.slots + slot) * g.n_tiles + tile;
+    stride = (int64_t)g.n_tiles * R;
+  }
   const int n_s = max(1, (steps + per - 1) / per);     // splits that had tokens
-  const int64_t unit = ((int64_t)blockIdx.z * gridDim.y + h) * g.n_tiles + tile;
   for (int i = threadIdx.x; i < RB * (D / 4); i += 128) {
     const int r = r_lo + i / (D / 4), c = (i % (D / 4)) * 4;
     if (row0 + r >= nrows) continue;
-    const int64_t at0 = unit * g.n_split * R + r;
+    const int64_t at0 = part0 * R + r;
     float M = -INFINITY, S = 0.f;
-    for (int s = 0; s < n_s; ++s) M = fmaxf(M, g.part_ml[at0 + (int64_t)s * R].x);
+    for (int s = 0; s < n_s; ++s) M = fmaxf(M, g.part_ml[at0 + s * stride].x);
     const float use = M == -INFINITY ? 0.f : M;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int s = 0; s < n_s; ++s) {
-      const int64_t at = at0 + (int64_t)s * R;
+      const int64_t at = at0 + s * stride;
       const float2 ml = g.part_ml[at];
       const float f = tc::ex2(ml.x - use);
       const float4 v = *reinterpret_cast<const float4*>(g.part_o + at * D + c);

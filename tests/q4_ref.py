@@ -55,15 +55,15 @@ def tolerance(dtype, o, mag_v, mag_s, all_v, tc=False):
     |s| <= mag_s, in both) and 2^x is good to 2^-22.  A weight is off by that in
     its numerator and in the sum, so 2 (es + 2^-21); P is rounded to fp16 (2^-11; fp32: two
     parts, 2^-21), sums of P V add 2^-20.  The output is rounded once.
-    P is 2^15 e, e relative to the largest.  What is below fp16's smallest
-    normal value is held to a multiple of 2^-24, so every weight may be off by
-    2^-25 too, which is 2^-40 of the largest: 2^-40 all_v.
+    P is 2^11 e, e relative to a maximum at most the largest score.  What is
+    below fp16's smallest normal value is held to a multiple of 2^-24, so every
+    weight may be off by 2^-25 too: 2^-36 all_v.
     tc, the kernel for many query rows: P is 2^7 e, so 2^-32 all_v; 6 of 16
     exponentials are a polynomial good to 7.8e-5, in numerator and sum."""
     out = {"bf16": 2.0 ** -8, "fp32": 2.0 ** -24}[dtype]
     p = {"bf16": 2.0 ** -11, "fp32": 2.0 ** -21}[dtype]
     es = 42 * 2.0 ** -23 * mag_s
-    poly, small = (7.8e-5, 2.0 ** -32) if tc else (0.0, 2.0 ** -40)
+    poly, small = (7.8e-5, 2.0 ** -32) if tc else (0.0, 2.0 ** -36)
     rel = 2 * (es + 2.0 ** -21 + poly) + p + 2.0 ** -20
     to = (rel[..., None] * mag_v + small * all_v) * (1 + out) + out * np.abs(o) + 1e-30
     return to, 2 * es + poly + 2.0 ** -20 + 2.0 ** -22 * 40
