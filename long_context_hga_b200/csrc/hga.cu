@@ -1179,7 +1179,9 @@ hga_status q4_cache(const hga_params* p, const hga_page_pool* pool, int32_t plan
   if (pool->page_bytes != need) return HGA_ERR_INVALID_ARG;
   *c = hga::Q4Cache{static_cast<char*>(pool->data) + plane * pool->plane_stride, pool->page_bytes,
                     pool->table, pool->len, pool->n_pages, pool->n_rows, pool->row_pages,
-                    pool->page_tokens / 8, pool->page_tokens, p->n_kv_heads};
+                    pool->page_tokens / 8, pool->page_tokens, p->n_kv_heads, 0};
+  const uint64_t d = pool->page_tokens / 8;
+  c->page_recs_inv = (uint32_t)std::min<uint64_t>(((1ull << 32) + d - 1) / d, 0xffffffffull);
   return HGA_OK;
 }
 
@@ -1249,7 +1251,8 @@ Q4Plan q4_plan(const hga_params* p, int64_t units, int64_t rows, int64_t max_tok
   // heads on 4: one wave 79 us, two 91, three 105); a split has at least one
   // step for every warp
   const int64_t wave = 148 * (p->dtype == HGA_BF16 && pl.rows == 8 ? 3 : 2);
-  const int64_t most = (max_tok + 64 * hga::kQ4Warps - 1) / (64 * hga::kQ4Warps);
+  const int64_t cta_tok = hga::kQ4StepTok * hga::kQ4Warps;
+  const int64_t most = (max_tok + cta_tok - 1) / cta_tok;
   if (most <= 1) return pl;
   if (n_seq > 0) {
     const int64_t slots = std::min(wave / ((int64_t)p->n_kv_heads * pl.n_tiles), n_seq * most);
@@ -1267,7 +1270,7 @@ int64_t q4_work_bytes(const hga_params* p, int64_t parts, int rows) {
 template <int D, int R, int ENT, typename T, bool ROUTED>
 hga_status launch_q4_join(const hga::Q4AttendArgs& g, int64_t nz, cudaStream_t st) {
   return launch_pdl(hga::q4_join_kernel<D, R, ENT, T, ROUTED>,
-                    dim3((unsigned)(g.n_tiles * (R > 16 ? R / 16 : 1)), g.a.Hkv, (unsigned)nz),
+                    dim3((unsigned)(g.n_tiles * (R > 16 ? R / 16 : R)), g.a.Hkv, (unsigned)nz),
                     dim3(128), 0, st, g);
 }
 
@@ -1295,7 +1298,7 @@ hga_status launch_q4_attend(hga::Q4AttendArgs& g, int64_t nz, cudaStream_t st) {
   s = launch_pdl(hga::q4_attend_kernel<D, NT, T, ROUTED>, grid, dim3(32 * hga::kQ4Warps), smem, st,
                  g);
   if (s != HGA_OK || (g.n_split == 1 && !g.slots)) return s;
-  return launch_q4_join<D, 8 * NT, 8, T, ROUTED>(g, nz, st);
+  return launch_q4_join<D, 8 * NT, hga::kQ4StepRecs, T, ROUTED>(g, nz, st);
 }
 
 template <bool ROUTED>

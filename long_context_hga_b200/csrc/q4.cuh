@@ -32,6 +32,7 @@ struct Q4Cache {
   const int32_t* table;      // [n_rows][row_pages]
   const int32_t* len;        // [n_rows]
   int n_pages, n_rows, row_pages, page_recs, page_tokens, Hkv;
+  uint32_t page_recs_inv;    // 2^32 / page_recs, rounded up (page_recs = 1: 2^32 - 1)
 };
 
 struct Q4BatchArgs {

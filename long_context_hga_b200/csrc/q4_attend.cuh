@@ -29,7 +29,8 @@
 namespace hga {
 
 constexpr int kQ4Warps = 4;
-constexpr int kQ4StepTok = 64;            // tokens a warp takes at a time
+constexpr int kQ4StepRecs = 8;            // records of 8 tokens a warp takes at a time
+constexpr int kQ4StepTok = 8 * kQ4StepRecs;
 // Weights are held as 2^11 times exp(score - m), m a maximum that is only moved
 // when a score passes it by more than 2^4: at most 2^15 in fp16, with 11 bits
 // down to 2^-25 of the largest one (fp16's subnormals start at 2^-14).
@@ -56,7 +57,7 @@ template <int D, int NT, bool ROUTED>
 struct Q4Layout {
   static constexpr int kStages = 2;
   static constexpr int kRec = q4_record_bytes(D);
-  static constexpr int kStage = 8 * kRec;
+  static constexpr int kStage = kQ4StepRecs * kRec;
   static constexpr int kRingOff = 0;
   static constexpr int kRing = kQ4Warps * kStages * kStage;
   static constexpr int kJoin = kQ4Warps * 8 * NT * (D + 2) * 4;     // reuses the ring
@@ -203,7 +204,10 @@ __device__ __forceinline__ int q4_entry(const Q4List& x, int i) {
 // page table names none.
 __device__ __forceinline__ int64_t q4_where(const Q4Cache& c, const int32_t* pages, int h, int ent,
                                             int rec_bytes) {
-  const int col = ent / c.page_recs, in = ent - col * c.page_recs;
+  // ent / page_recs by the reciprocal, off by at most one
+  int col = (int)__umulhi((uint32_t)ent, c.page_recs_inv), in = ent - col * c.page_recs;
+  if (in < 0) --col, in += c.page_recs;
+  else if (in >= c.page_recs) ++col, in -= c.page_recs;
   const int pg = col < c.row_pages ? pages[col] : -1;
   if (pg < 0 || pg >= c.n_pages) {
     report(HGA_ERR_DEVICE_CHECK);
@@ -239,7 +243,8 @@ __device__ __forceinline__ int q4_seq_steps(const Q4AttendArgs& g, int z) {
   const int r = g.b.rows[z];
   if (r < 0 || r >= g.c.n_rows) return 0;
   const int ctx = g.c.len[r];
-  return ctx <= 0 || ctx > (int64_t)g.c.row_pages * g.c.page_tokens ? 0 : (ctx + 63) / 64;
+  return ctx <= 0 || ctx > (int64_t)g.c.row_pages * g.c.page_tokens ? 0
+                                                                        : (ctx + kQ4StepTok - 1) / kQ4StepTok;
 }
 __device__ __forceinline__ int q4_deal(const Q4AttendArgs& g, int lane) {
   int64_t total = 0;
@@ -276,7 +281,7 @@ __device__ __forceinline__ bool q4_dealt(const Q4AttendArgs& g, int per, int lan
   return false;
 }
 
-// Steps of 64 tokens (or 8 list entries) of one split.
+// Steps of one split.
 __device__ __forceinline__ void q4_split_range(int steps, int n_split, int split, int* lo, int* hi) {
   const int per = (steps + n_split - 1) / n_split;
   *lo = min(steps, split * per);
@@ -296,6 +301,7 @@ __global__ void __launch_bounds__(32 * kQ4Warps, (q4_ctas<NT, T>())) q4_attend_k
   constexpr bool kSplitFp = sizeof(T) == 4;     // fp32: q and P as sums of two fp16 values
   constexpr int KS = D / 16;                    // k-steps of S, m-tiles of O
   constexpr int R = 8 * NT;
+  constexpr int kMt = kQ4StepRecs / 2;          // 16-token tiles of a step
   extern __shared__ __align__(128) char smem[];
   __shared__ int s_abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -330,7 +336,7 @@ __global__ void __launch_bounds__(32 * kQ4Warps, (q4_ctas<NT, T>())) q4_attend_k
   const int first_pos = u.pos0 + row0 / g.a.G;
   const Q4List list = q4_list<ROUTED>(g, u, z, h, first_pos, last_pos);
   const int n_ent = list.n;
-  const int steps = (n_ent + 7) / 8;
+  const int steps = (n_ent + kQ4StepRecs - 1) / kQ4StepRecs;
   int lo, hi;
   if (per) {
     lo = min(steps, split * per);
@@ -346,15 +352,24 @@ __global__ void __launch_bounds__(32 * kQ4Warps, (q4_ctas<NT, T>())) q4_attend_k
   const int n_mine = hi > lo + warp ? (hi - lo - warp + kQ4Warps - 1) / kQ4Warps : 0;
   unsigned got[kQ4Stages];                      // records that were fetched, per stage
   int issued = 0;
+  int ent = -1;                                 // this lane's record of the next fetch
+  int64_t at = -1;
+  auto look = [&](int i) {
+    ent = i < n_mine && lane < kQ4StepRecs
+              ? q4_entry<ROUTED>(list, (lo + warp + i * kQ4Warps) * kQ4StepRecs + lane)
+              : -1;
+    at = ent >= 0 ? q4_where(g.c, pages, h, ent, L::kRec) : -1;
+  };
+  // Fetches step i; its places were looked up during the step before.
   auto fetch = [&](int i, int s) -> unsigned {
-    int ent = lane < 8 ? q4_entry<ROUTED>(list, (lo + warp + i * kQ4Warps) * 8 + lane) : -1;
-    const int64_t at = ent >= 0 ? q4_where(g.c, pages, h, ent, L::kRec) : -1;
-    if (lane < 8) ents[s * 8 + lane] = at >= 0 ? ent : -1;
+    if (lane < kQ4StepRecs) ents[s * 8 + lane] = at >= 0 ? ent : -1;
     const unsigned m = __ballot_sync(0xffffffffu, at >= 0);
     ++issued;
     q4_fetch8(ring + s * L::kStage, g.c.base, at, L::kRec, &bars[s], lane);
+    look(i + 1);
     return m;
   };
+  look(0);
 #pragma unroll
   for (int s = 0; s < kQ4Stages; ++s) got[s] = s < n_mine ? fetch(s, s) : 0;
 
@@ -424,13 +439,13 @@ __global__ void __launch_bounds__(32 * kQ4Warps, (q4_ctas<NT, T>())) q4_attend_k
     unsigned have = got[0];
 #pragma unroll
     for (int x = 1; x < kQ4Stages; ++x) if (s == x) have = got[x];
-    const int e0 = (lo + warp + i * kQ4Warps) * 8;
-    const bool edge = have != 0xffu || e0 + 8 > list.n_whole;
+    const int e0 = (lo + warp + i * kQ4Warps) * kQ4StepRecs;
+    const bool edge = have != (1u << kQ4StepRecs) - 1 || e0 + kQ4StepRecs > list.n_whole;
     const int* ent_of = ents + s * 8;
     // ---- scores
-    float sv[4][NT][4];
+    float sv[kMt][NT][4];
 #pragma unroll
-    for (int mt = 0; mt < 4; ++mt) {
+    for (int mt = 0; mt < kMt; ++mt) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -479,7 +494,7 @@ __global__ void __launch_bounds__(32 * kQ4Warps, (q4_ctas<NT, T>())) q4_attend_k
     // ---- mask: tokens past the row's position and records that are not there
     if (edge) {
 #pragma unroll
-      for (int mt = 0; mt < 4; ++mt)
+      for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
           const int rec = 2 * mt + y;
@@ -493,10 +508,10 @@ __global__ void __launch_bounds__(32 * kQ4Warps, (q4_ctas<NT, T>())) q4_attend_k
               if (!there || tok > pos[nt][x]) sv[mt][nt][2 * y + x] = -INFINITY;
         }
     }
-    // ---- softmax over the step's 64 tokens.  m is a score, not yet scaled: the
+    // ---- softmax over the step's tokens.  m is a score, not yet scaled: the
     // difference to it is taken first, so that it stays <= 0 however large
     // scores are
-    uint32_t ph[4][NT][2], pl[kSplitFp ? 4 : 1][NT][2];
+    uint32_t ph[kMt][NT][2], pl[kSplitFp ? kMt : 1][NT][2];
     float top[NT][2];
     bool grow = false;
 #pragma unroll
@@ -505,7 +520,7 @@ __global__ void __launch_bounds__(32 * kQ4Warps, (q4_ctas<NT, T>())) q4_attend_k
       for (int x = 0; x < 2; ++x) {
         float mx = -INFINITY;
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt) mx = fmaxf(mx, fmaxf(sv[mt][nt][x], sv[mt][nt][2 + x]));
+        for (int mt = 0; mt < kMt; ++mt) mx = fmaxf(mx, fmaxf(sv[mt][nt][x], sv[mt][nt][2 + x]));
         top[nt][x] = mx;
         grow |= m[nt][x] == -INFINITY ? mx > -INFINITY : (mx - m[nt][x]) * sc[nt][x] > kQ4Grow;
       }
@@ -535,7 +550,7 @@ __global__ void __launch_bounds__(32 * kQ4Warps, (q4_ctas<NT, T>())) q4_attend_k
         const float use = m[nt][x] == -INFINITY ? 0.f : m[nt][x];
         float sum = 0.f;
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt)
+        for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
             float& p = sv[mt][nt][2 * y + x];
@@ -545,7 +560,7 @@ __global__ void __launch_bounds__(32 * kQ4Warps, (q4_ctas<NT, T>())) q4_attend_k
         l[nt][x] += sum;
       }
 #pragma unroll
-      for (int mt = 0; mt < 4; ++mt)
+      for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
           if constexpr (kSplitFp) {
@@ -559,7 +574,7 @@ __global__ void __launch_bounds__(32 * kQ4Warps, (q4_ctas<NT, T>())) q4_attend_k
     }
     // ---- O^T += V^T P^T
 #pragma unroll
-    for (int mt = 0; mt < 4; ++mt) {
+    for (int mt = 0; mt < kMt; ++mt) {
       // tokens k = 2t, 2t + 1 (record 2mt, tokens t and t + 4) and 2t + 8, 2t + 9
       uint32_t w[4][D / 64], sab, scd;
       const char* rec = st + (2 * mt) * L::kRec + 4 * D;
@@ -687,12 +702,18 @@ __global__ void __launch_bounds__(32 * kQ4Warps, (q4_ctas<NT, T>())) q4_attend_k
   griddep_launch();
 }
 
-// Joins the splits of each unit's rows, in split order.  R: rows of a tile, of
-// which a block takes at most 16; ENT: entries of a split's step.
+// Joins the splits of each unit's rows, in a fixed order.  R: rows of a tile,
+// ENT: entries of a split's step.  Few rows (many splits each): a block of four
+// warps joins one row, a warp every fourth split.  256 rows (few splits): 16
+// rows a block, four for each warp.
 template <int D, int R, int ENT, typename T, bool ROUTED>
 __global__ void __launch_bounds__(128) q4_join_kernel(const Q4AttendArgs g) {
-  constexpr int RB = R < 16 ? R : 16;
+  constexpr int RB = R > 16 ? 16 : 1;
+  constexpr int W = RB == 1 ? 4 : 1;            // warps of a row
+  constexpr int V = D / 32;                     // values of a lane
+  __shared__ float s_acc[4][D + 1];
   griddep_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int tile = blockIdx.x / (R / RB), r_lo = blockIdx.x % (R / RB) * RB, h = blockIdx.y;
   Q4Unit u;
   const int z = blockIdx.z + (ROUTED ? g.z0 : 0);
@@ -706,38 +727,61 @@ __global__ void __launch_bounds__(128) q4_join_kernel(const Q4AttendArgs g) {
   int64_t part0 = (((int64_t)blockIdx.z * gridDim.y + h) * g.n_tiles + tile) * g.n_split, stride = R;
   if (!ROUTED && g.slots) {
     int slot = 0, zz;
-    per = q4_deal(g, threadIdx.x & 31);
+    per = q4_deal(g, lane);
     if (steps <= per) return;                          // already whole
-    q4_dealt(g, per, threadIdx.x & 31, z, &slot, &zz);
+    q4_dealt(g, per, lane, z, &slot, &zz);
     part0 = ((int64_t)h * g.slots + slot) * g.n_tiles + tile;
     stride = (int64_t)g.n_tiles * R;
   }
   const int n_s = max(1, (steps + per - 1) / per);     // splits that had tokens
-  for (int i = threadIdx.x; i < RB * (D / 4); i += 128) {
-    const int r = r_lo + i / (D / 4), c = (i % (D / 4)) * 4;
-    if (row0 + r >= nrows) continue;
+  for (int r = r_lo + (W == 1 ? warp : 0); r < r_lo + RB && row0 + r < nrows; r += 4 / W) {
     const int64_t at0 = part0 * R + r;
-    float M = -INFINITY, S = 0.f;
-    for (int s = 0; s < n_s; ++s) M = fmaxf(M, g.part_ml[at0 + s * stride].x);
+    float M = -INFINITY;
+    for (int s = lane; s < n_s; s += 32) M = fmaxf(M, g.part_ml[at0 + s * stride].x);
+    M = warp_max(M);
     const float use = M == -INFINITY ? 0.f : M;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s = 0; s < n_s; ++s) {
+    float acc[V], S = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = 0.f;
+#pragma unroll 4
+    for (int s = W == 1 ? 0 : warp; s < n_s; s += W) {
       const int64_t at = at0 + s * stride;
       const float2 ml = g.part_ml[at];
       const float f = tc::ex2(ml.x - use);
-      const float4 v = *reinterpret_cast<const float4*>(g.part_o + at * D + c);
       S += ml.y * f;
-      acc.x += v.x * f; acc.y += v.y * f; acc.z += v.z * f; acc.w += v.w * f;
+      const float* src = g.part_o + at * D + lane * V;
+      float v[V];
+      if constexpr (V == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(src);
+        v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+      } else {
+        const float2 x = *reinterpret_cast<const float2*>(src);
+        v[0] = x.x; v[1] = x.y;
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] += v[i] * f;
+    }
+    if constexpr (W > 1) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) s_acc[warp][lane * V + i] = acc[i];
+      if (lane == 0) s_acc[warp][D] = S;
+      __syncthreads();
+      if (warp > 0) return;
+      S = 0.f;
+      for (int w = 0; w < 4; ++w) S += s_acc[w][D];
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        acc[i] = (s_acc[0][lane * V + i] + s_acc[1][lane * V + i]) +
+                 (s_acc[2][lane * V + i] + s_acc[3][lane * V + i]);
     }
     const float inv = S > 0.f ? 1.f / S : 0.f;
     const int pr = row0 + r;
     const int64_t orow = (u.tok0 + pr / g.a.G) * g.a.Hq + (int64_t)h * g.a.G + pr % g.a.G;
-    T* dst = static_cast<T*>(g.a.o) + orow * D + c;
-    dst[0] = Elt<T>::from_f32(acc.x * inv);
-    dst[1] = Elt<T>::from_f32(acc.y * inv);
-    dst[2] = Elt<T>::from_f32(acc.z * inv);
-    dst[3] = Elt<T>::from_f32(acc.w * inv);
-    if (c == 0 && g.a.lse) g.a.lse[orow] = S > 0.f ? (M + (log2f(S) - g.shift)) * 0.6931471805599453f : -INFINITY;
+    T* dst = static_cast<T*>(g.a.o) + orow * D + lane * V;
+#pragma unroll
+    for (int i = 0; i < V; ++i) dst[i] = Elt<T>::from_f32(acc[i] * inv);
+    if (lane == 0 && g.a.lse)
+      g.a.lse[orow] = S > 0.f ? (M + (log2f(S) - g.shift)) * 0.6931471805599453f : -INFINITY;
   }
   griddep_launch();
 }
