@@ -1114,7 +1114,10 @@ hga_status rope_common(const hga_rope_plan* r, const int32_t* pos, int64_t pos_s
   a.adjacent = r->adjacent;
   a.heads0 = q->heads;
   a.heads = q->heads + (k ? k->heads : 0);
-  a.toks = n >= 148 * 8 ? 4 : 1;
+  // about 2048 blocks, fewer tokens in each of a shorter call (4096 tokens, 40
+  // heads of 128: 2 tokens a block 35 us, 8 tokens 43; 16384: 8 tokens 70, 2
+  // tokens 74)
+  a.toks = (int)std::max<int64_t>(1, std::min<int64_t>(8, n / 2048));
   a.sign = sign;
   if (q->in_dtype == HGA_BF16)
     return q->out_dtype == HGA_BF16 ? launch_rope_vec<__nv_bfloat16, __nv_bfloat16>(a, vec, st)
@@ -1200,6 +1203,7 @@ hga_status q4_io_args(const hga_params* p, const hga_page_pool* pool, int32_t pl
   if (s != HGA_OK) return s;
   if ((s = check_batch(b, n_tok)) != HGA_OK) return s;
   if (n_tok == 0 || b->n_seq == 0) return HGA_OK;
+  if (n_tok > 0x7fffffff) return HGA_ERR_UNSUPPORTED;
   if (!k || !v || !aligned16(k) || !aligned16(v)) return HGA_ERR_INVALID_ARG;
   if ((kt * ke) % 16 || (kh * ke) % 16 || (vt * ve) % 16 || (vh * ve) % 16)
     return HGA_ERR_INVALID_ARG;
@@ -1215,9 +1219,10 @@ hga_status q4_io_args(const hga_params* p, const hga_page_pool* pool, int32_t pl
   return HGA_OK;
 }
 
-unsigned q4_io_grid(const hga::Q4IoArgs& a) {
-  const int64_t total = a.n_tok * a.c.Hkv * (a.D / 16);
-  return (unsigned)std::min<int64_t>((total + hga::kQ4Threads - 1) / hga::kQ4Threads, 1 << 20);
+// Tokens of a block, and blocks.
+unsigned q4_io_grid(hga::Q4IoArgs* a) {
+  a->toks = (int)std::max<int64_t>(1, std::min<int64_t>(hga::kQ4BlockTok, a->n_tok / (148 * 16)));
+  return (unsigned)((a->n_tok + a->toks - 1) / a->toks);
 }
 
 // ---------------------------------------------------------------- 4-bit attention
@@ -1403,11 +1408,7 @@ hga_status hga_pages_compact(const hga_page_pool* pool, hga_stream_t stream) {
   if ((s = launch_pdl(hga::pages_compact_plan_kernel, dim3(1), dim3(hga::kPlanThreads), 0, st,
                       a)) != HGA_OK)
     return s;
-  if ((s = launch_pdl(hga::pages_compact_kernel, dim3(copy_grid(a, pool->n_pages)),
-                      dim3(hga::kCopyThreads), 0, st, a)) != HGA_OK)
-    return s;
-  return launch_pdl(hga::pages_compact_ref_kernel,
-                    dim3((unsigned)std::min((pool->n_pages + 255) / 256, 148)),
+  return launch_pdl(hga::pages_compact_kernel, dim3(copy_grid(a, pool->n_pages)),
                     dim3(hga::kCopyThreads), 0, st, a);
 }
 
@@ -1441,11 +1442,12 @@ hga_status hga_q4_append(const hga_params* p, const hga_page_pool* pool, int32_t
   hga_status s = q4_io_args(p, pool, plane, b, n_tok, k, k_token_stride, k_head_stride, v,
                             v_token_stride, v_head_stride, e, e, &a);
   if (s != HGA_OK || n_tok == 0 || b->n_seq == 0) return s;
+  const dim3 grid(q4_io_grid(&a));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return p->dtype == HGA_BF16
-             ? launch_pdl(hga::q4_append_kernel<__nv_bfloat16>, dim3(q4_io_grid(a)),
+             ? launch_pdl(hga::q4_append_kernel<__nv_bfloat16>, grid,
                           dim3(hga::kQ4Threads), 0, st, a)
-             : launch_pdl(hga::q4_append_kernel<float>, dim3(q4_io_grid(a)),
+             : launch_pdl(hga::q4_append_kernel<float>, grid,
                           dim3(hga::kQ4Threads), 0, st, a);
 }
 
@@ -1459,7 +1461,7 @@ hga_status hga_q4_read(const hga_params* p, const hga_page_pool* pool, int32_t p
                             v_token_stride, v_head_stride, e, e, &a);
   if (s != HGA_OK || n_tok == 0 || b->n_seq == 0) return s;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const dim3 grid(q4_io_grid(a)), block(hga::kQ4Threads);
+  const dim3 grid(q4_io_grid(&a)), block(hga::kQ4Threads);
   if (p->dtype == HGA_FP32)
     return launch_pdl(hga::q4_read_kernel<float, float>, grid, block, 0, st, a);
   return p->v_f16 ? launch_pdl(hga::q4_read_kernel<__nv_bfloat16, __half>, grid, block, 0, st, a)

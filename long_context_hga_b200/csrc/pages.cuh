@@ -249,7 +249,7 @@ __device__ __forceinline__ void copy_pages(const PoolArgs& a, const int32_t* src
     const int64_t at = piece * kPiece + threadIdx.x;
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      if (at + k * kCopyThreads < vecs) v[k] = __ldcs(from + at + k * kCopyThreads);
+      if (at + k * kCopyThreads < vecs) v[k] = from[at + k * kCopyThreads];
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       if (at + k * kCopyThreads < vecs) __stcs(to + at + k * kCopyThreads, v[k]);
@@ -290,7 +290,8 @@ __global__ void __launch_bounds__(kCopyThreads) pages_fork_kernel(PoolArgs a,
 // ---------------------------------------------------------------- compact
 
 // wa: used pages at or above the used count, wb: free pages below it (as many,
-// both ascending), wc[page] = where a moved page goes.
+// both ascending), wc[page] = where a page at or above the count goes, -1 for a
+// free one.  The counts move here; the table follows wc.
 __global__ void __launch_bounds__(kPlanThreads) pages_compact_plan_kernel(PoolArgs a) {
   griddep_wait();
   int used = 0;
@@ -307,9 +308,18 @@ __global__ void __launch_bounds__(kPlanThreads) pages_compact_plan_kernel(PoolAr
   }
   const int moves = list_pages(a.ref, used, a.n_pages, true, a.wa, a.n_pages);
   list_pages(a.ref, 0, used, false, a.wb, a.n_pages);
-  if (threadIdx.x == 0) a.count[0] = moves;
-  for (int j = threadIdx.x; j < moves; j += kPlanThreads) a.wc[a.wa[j]] = a.wb[j];
-  if (threadIdx.x == 0) a.count[1] = used;
+  if (threadIdx.x == 0) {
+    a.count[0] = moves;
+    a.count[1] = used;
+  }
+  for (int i = used + threadIdx.x; i < a.n_pages; i += kPlanThreads) a.wc[i] = -1;
+  __syncthreads();
+  for (int j = threadIdx.x; j < moves; j += kPlanThreads) {
+    const int from = a.wa[j], to = a.wb[j];
+    a.wc[from] = to;
+    a.ref[to] = a.ref[from];
+    a.ref[from] = 0;
+  }
   griddep_launch();
 }
 
@@ -321,24 +331,11 @@ __global__ void __launch_bounds__(kCopyThreads) pages_compact_kernel(PoolArgs a)
   for (int64_t i = tid; i < (int64_t)a.n_rows * a.row_pages; i += nthr) {
     const int pg = a.table[i];
     if (pg < used) continue;
-    if (pg >= a.n_pages || a.ref[pg] == 0) {
-      // an entry that names no page of the pool, or a free one
-      report(HGA_ERR_DEVICE_CHECK);
-      continue;
-    }
-    a.table[i] = a.wc[pg];
+    const int to = pg < a.n_pages ? a.wc[pg] : -1;
+    if (to >= 0) a.table[i] = to;
+    else report(HGA_ERR_DEVICE_CHECK);    // no page of the pool, or a free one
   }
   copy_pages(a, a.wa, a.wb, moves, blockIdx.x, gridDim.x);
-}
-
-// The counts move last: the kernel above still reads them.
-__global__ void __launch_bounds__(kCopyThreads) pages_compact_ref_kernel(PoolArgs a) {
-  griddep_wait();
-  const int moves = a.count[0];
-  for (int j = blockIdx.x * kCopyThreads + threadIdx.x; j < moves; j += gridDim.x * kCopyThreads) {
-    a.ref[a.wb[j]] = a.ref[a.wa[j]];
-    a.ref[a.wa[j]] = 0;
-  }
 }
 
 // ---------------------------------------------------------------- copy

@@ -176,6 +176,7 @@ __device__ __forceinline__ uint32_t q4_mul2(uint32_t a, uint32_t b) {
 // ---------------------------------------------------------------- append
 
 constexpr int kQ4Threads = 256;
+constexpr int kQ4BlockTok = 32;             // most tokens of a block
 
 struct Q4IoArgs {
   Q4Cache c;
@@ -183,6 +184,7 @@ struct Q4IoArgs {
   const void *k, *v;         // append: the tokens; read: where they go
   int64_t k_tok, k_head, v_tok, v_head;   // strides in elements
   int64_t n_tok;
+  int toks;                  // tokens of a block
   int D;
 };
 
@@ -205,34 +207,51 @@ __device__ __forceinline__ void q4_load16(const T* p, float* f) {
   }
 }
 
+// A block's tokens: where their records are, looked up once by one thread each
+// (a thread of the loop below handles 16 values, for which the search of the
+// sequence and the page would cost more than the values).  off < 0: no token.
+struct Q4BlockTokens {
+  int64_t off[kQ4BlockTok];  // the record of KV head 0, in bytes from the plane's first page
+  int r[kQ4BlockTok];        // row within the record
+};
+__device__ __forceinline__ void q4_block_tokens(const Q4IoArgs& a, int64_t t0, int nt,
+                                                Q4BlockTokens* s) {
+  for (int i = threadIdx.x; i < nt; i += kQ4Threads) {
+    int row, pos;
+    char* rec = nullptr;
+    if (q4_locate(a.c, a.b, t0 + i, &row, &pos)) rec = q4_record(a.c, row, pos, 0, q4_record_bytes(a.D));
+    s->off[i] = rec ? rec - a.c.base : -1;
+    s->r[i] = pos & 7;
+  }
+  __syncthreads();
+}
+
 // One thread per 16 values of K and the same 16 of V: the maximum needs no
 // exchange between threads.  Bound: HBM (reads 4 d, writes 9 d / 8 bytes per
 // token and head).
 template <typename T>
 __global__ void __launch_bounds__(kQ4Threads) q4_append_kernel(const Q4IoArgs a) {
+  __shared__ Q4BlockTokens tok;
   griddep_wait();
-  const int nb = a.D >> 4;                          // scale blocks of a head's row
-  const int64_t total = a.n_tok * a.c.Hkv * nb;
+  const int64_t t0 = (int64_t)blockIdx.x * a.toks;
+  const int nt = (int)min((int64_t)a.toks, a.n_tok - t0);
+  q4_block_tokens(a, t0, nt, &tok);
+  const int nb = a.D >> 4, log_nb = a.D == 128 ? 3 : 2;   // scale blocks of a head's row
+  const int hb = a.c.Hkv << log_nb;
   bool bad = false;
   // a row named by two sequences of the call would be written twice: reported
-  if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i < a.b.n_seq; i += kQ4Threads)
-      for (int j = 0; j < i; ++j)
-        if (a.b.rows[i] >= 0 && a.b.rows[j] == a.b.rows[i]) bad = true;
-  for (int64_t i = (int64_t)blockIdx.x * kQ4Threads + threadIdx.x; i < total;
-       i += (int64_t)gridDim.x * kQ4Threads) {
-    const int blk = (int)(i % nb);
-    const int64_t th = i / nb;
-    const int h = (int)(th % a.c.Hkv);
-    const int64_t tok = th / a.c.Hkv;
-    int row, pos;
-    if (!q4_locate(a.c, a.b, tok, &row, &pos)) continue;
-    char* rec = q4_record(a.c, row, pos, h, q4_record_bytes(a.D));
-    if (!rec) continue;
-    const int r = pos & 7;
+  for (int i = blockIdx.x * kQ4Threads + threadIdx.x; i < a.b.n_seq; i += gridDim.x * kQ4Threads)
+    for (int j = 0; j < i; ++j)
+      if (a.b.rows[i] >= 0 && a.b.rows[j] == a.b.rows[i]) bad = true;
+  const int dt = kQ4Threads / hb, dx = kQ4Threads % hb;
+  int t = threadIdx.x / hb, x = threadIdx.x % hb;
+  for (; t < nt; t += dt + (x + dx >= hb), x = x + dx >= hb ? x + dx - hb : x + dx) {
+    if (tok.off[t] < 0) continue;
+    const int h = x >> log_nb, blk = x & (nb - 1), r = tok.r[t];
+    char* rec = a.c.base + tok.off[t] + (int64_t)h * a.c.page_recs * q4_record_bytes(a.D);
     float k[16], v[16];
-    q4_load16(static_cast<const T*>(a.k) + tok * a.k_tok + h * a.k_head + blk * 16, k);
-    q4_load16(static_cast<const T*>(a.v) + tok * a.v_tok + h * a.v_head + blk * 16, v);
+    q4_load16(static_cast<const T*>(a.k) + (t0 + t) * a.k_tok + h * a.k_head + blk * 16, k);
+    q4_load16(static_cast<const T*>(a.v) + (t0 + t) * a.v_tok + h * a.v_head + blk * 16, v);
     int ks, vs;
     const uint2 kc = q4_encode<T>(k, &ks, &bad);
     const uint2 vc = q4_encode<T>(v, &vs, &bad);
@@ -281,26 +300,25 @@ __device__ __forceinline__ void q4_decode16(const uint2 codes, int scale, T* out
 
 template <typename TK, typename TV>
 __global__ void __launch_bounds__(kQ4Threads) q4_read_kernel(const Q4IoArgs a) {
+  __shared__ Q4BlockTokens tok;
   griddep_wait();
-  const int nb = a.D >> 4, half = a.D >> 1;
-  const int64_t total = a.n_tok * a.c.Hkv * nb;
-  for (int64_t i = (int64_t)blockIdx.x * kQ4Threads + threadIdx.x; i < total;
-       i += (int64_t)gridDim.x * kQ4Threads) {
-    const int blk = (int)(i % nb);
-    const int64_t th = i / nb;
-    const int h = (int)(th % a.c.Hkv);
-    const int64_t tok = th / a.c.Hkv;
-    int row, pos;
-    if (!q4_locate(a.c, a.b, tok, &row, &pos)) continue;
-    const char* rec = q4_record(a.c, row, pos, h, q4_record_bytes(a.D));
-    if (!rec) continue;
-    const int r = pos & 7;
+  const int64_t t0 = (int64_t)blockIdx.x * a.toks;
+  const int nt = (int)min((int64_t)a.toks, a.n_tok - t0);
+  q4_block_tokens(a, t0, nt, &tok);
+  const int nb = a.D >> 4, log_nb = a.D == 128 ? 3 : 2, half = a.D >> 1;
+  const int hb = a.c.Hkv << log_nb;
+  const int dt = kQ4Threads / hb, dx = kQ4Threads % hb;
+  int t = threadIdx.x / hb, x = threadIdx.x % hb;
+  for (; t < nt; t += dt + (x + dx >= hb), x = x + dx >= hb ? x + dx - hb : x + dx) {
+    if (tok.off[t] < 0) continue;
+    const int h = x >> log_nb, blk = x & (nb - 1), r = tok.r[t];
+    const char* rec = a.c.base + tok.off[t] + (int64_t)h * a.c.page_recs * q4_record_bytes(a.D);
     const uint2 kc = *reinterpret_cast<const uint2*>(rec + r * half + blk * 8);
     const uint2 vc = *reinterpret_cast<const uint2*>(rec + 8 * half + r * half + blk * 8);
     const int ks = (unsigned char)rec[16 * half + r * nb + blk];
     const int vs = (unsigned char)rec[16 * half + 8 * nb + r * nb + blk];
-    q4_decode16(kc, ks, (TK*)a.k + tok * a.k_tok + h * a.k_head + blk * 16);
-    q4_decode16(vc, vs, (TV*)a.v + tok * a.v_tok + h * a.v_head + blk * 16);
+    q4_decode16(kc, ks, (TK*)a.k + (t0 + t) * a.k_tok + h * a.k_head + blk * 16);
+    q4_decode16(vc, vs, (TV*)a.v + (t0 + t) * a.v_tok + h * a.v_head + blk * 16);
   }
   griddep_launch();
 }

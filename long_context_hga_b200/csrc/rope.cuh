@@ -103,12 +103,17 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
     cs[t * a.half + p] = make_float2(c, a.sign * s);
   }
   __syncthreads();
-  // items of a head row: rotated vector pairs, then vectors past rot_dim
+  // Items of a head row: rotated vector pairs, then vectors past rot_dim.  A
+  // thread keeps its item and goes from row to row, so that the index
+  // arithmetic of a row is a few additions.
   const int rot_items = a.half / VEC, items = rot_items + (a.d - 2 * a.half) / VEC;
-  const int total = nt * a.heads * items;
-  for (int i = threadIdx.x; i < total; i += kRopeThreads) {
-    const int row = i / items, it = i - row * items;
-    const int t = row / a.heads, hh = row - t * a.heads;
+  const int rows = kRopeThreads / items;            // rows of a pass (items <= kRopeMaxDim)
+  const int it = threadIdx.x % items;
+  const int row = threadIdx.x / items;
+  int t = row < rows ? row / a.heads : nt, hh = row % a.heads;   // past them: no row
+  const int dt = rows / a.heads, dh = rows % a.heads;
+#pragma unroll 2
+  for (; t < nt; t += dt + (hh + dh >= a.heads), hh = hh + dh >= a.heads ? hh + dh - a.heads : hh + dh) {
     const RopeIo& io = a.io[hh >= a.heads0];
     const int h = hh >= a.heads0 ? hh - a.heads0 : hh;
     const TI* src = static_cast<const TI*>(io.in) + (t0 + t) * io.in_tok + h * io.in_head;

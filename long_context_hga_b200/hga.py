@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import dataclasses
 import os
+import struct
 import time
 from typing import Optional
 
@@ -77,6 +78,9 @@ class Params:
                        self.local, self.top_chunks, self.top_groups,
                        HGA_BF16 if self.dtype == "bf16" else HGA_FP32,
                        int(self.v_f16), int(self.q_ready))
+
+    def __getstate__(self):
+        return {k: v for k, v in self.__dict__.items() if k != "_ref"}   # see _cp
 
     @property
     def torch_dtype(self):
@@ -702,13 +706,13 @@ class CQ4Batch(ctypes.Structure):
 
 
 def _sig_serving():
-    P, R, IO = (ctypes.POINTER(c) for c in (CParams, CRopePlan, CRopeIo))
+    P, R = (ctypes.POINTER(c) for c in (CParams, CRopePlan))
     G, B = ctypes.POINTER(CPagePool), ctypes.POINTER(CQ4Batch)
     vp, i64, i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
     st = ctypes.c_int
     sig = {
-        "hga_rope": (st, [R, vp, i64, i64, IO, IO, vp]),
-        "hga_rope_backward": (st, [R, vp, i64, i64, IO, IO, vp]),
+        "hga_rope": (st, [R, vp, i64, i64, vp, vp, vp]),
+        "hga_rope_backward": (st, [R, vp, i64, i64, vp, vp, vp]),
         "hga_pages_work_ints": (i64, [G]),
         "hga_pages_reserve": (st, [G, vp, vp, i32, vp]),
         "hga_pages_fork": (st, [G, vp, vp, i32, vp]),
@@ -733,16 +737,29 @@ def _sig_serving():
 _sig_serving()
 
 _RAW_STREAM = torch._C._cuda_getCurrentRawStream
+_CURRENT_DEVICE = torch._C._cuda_getDevice
 
 
-def _on(what: str, stream, *tensors) -> int:
-    """The raw stream of a call whose tensors (None is skipped) must all be on
-    the current CUDA device; HgaError otherwise."""
-    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+# The calls below cost a few microseconds on the host, as much as a small kernel
+# on the GPU: their checks format no message and read no attribute twice.
+
+def _on(what: str, stream, dev: int, *tensors) -> int:
+    """The raw stream of a call on device dev (a tensor's), which must be the
+    current CUDA device and that of all the tensors (None is skipped)."""
+    if dev < 0 or dev != _CURRENT_DEVICE():
+        raise HgaError(HGA_ERR_INVALID_ARG, f"{what}: tensors must be on the current CUDA device")
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise HgaError(HGA_ERR_INVALID_ARG, f"{what}: tensors must be on the current CUDA device")
-    return _RAW_STREAM(dev) if stream is None else stream.cuda_stream
+    if stream is None:
+        return _RAW_STREAM(dev)
+    if stream.device_index != dev:
+        raise HgaError(HGA_ERR_INVALID_ARG, f"{what}: the stream is another device's")
+    return stream.cuda_stream
+
+
+def _bad(what: str):
+    raise HgaError(HGA_ERR_INVALID_ARG, what)
 
 
 def _want(ok: bool, what: str):
@@ -751,12 +768,12 @@ def _want(ok: bool, what: str):
 
 
 def _cp(p: Params):
-    """The C struct of a Params, built once (Params is immutable)."""
-    c = p.__dict__.get("_c")
+    """The C struct of a Params by reference, built once (Params is immutable)."""
+    c = p.__dict__.get("_ref")
     if c is None:
-        c = p.c()
-        object.__setattr__(p, "_c", c)
-    return ctypes.byref(c)
+        c = ctypes.byref(p.c())
+        object.__setattr__(p, "_ref", c)
+    return c
 
 
 _ROPE_DTYPES = {torch.bfloat16: HGA_BF16, torch.float32: HGA_FP32}
@@ -778,8 +795,11 @@ class Rope:
         if n_axes is None:
             n_axes = int(axis.max()) + 1 if axis.numel() else 1
         self.n_axes = n_axes
+        _want(axis.device == freq.device, "Rope: freq and axis are on one device")
+        self.dev = freq.get_device()
         self._c = CRopePlan(freq.data_ptr(), axis.data_ptr(), n_axes, head_dim, 2 * freq.numel(),
                             int(adjacent))
+        self._r = ctypes.byref(self._c)
 
     @staticmethod
     def make(head_dim: int, theta: float, sections=None, rot_dim: Optional[int] = None,
@@ -807,29 +827,38 @@ class Rope:
                     head_dim, n_axes=len(sections), adjacent=adjacent)
 
 
-def _rope_io(what: str, n: int, d: int, x, out):
-    _want(x.dim() == 3 and x.shape == out.shape and x.shape[0] == n and x.shape[2] == d
-          and (x.stride(2) == 1 or d == 1) and (out.stride(2) == 1 or d == 1),
-          f"{what}: tensors are [n, heads, head_dim] with contiguous heads")
-    _want(x.dtype in _ROPE_DTYPES and out.dtype in _ROPE_DTYPES, f"{what}: bf16 or fp32")
-    return CRopeIo(x.data_ptr(), out.data_ptr(), x.stride(0), x.stride(1), out.stride(0),
-                   out.stride(1), x.shape[1], _ROPE_DTYPES[x.dtype], _ROPE_DTYPES[out.dtype])
+_ROPE_IO = struct.Struct("@QQqqqqiii4x")      # hga_rope_io
+
+
+def _rope_io(what: str, n: int, d: int, x, out) -> bytes:
+    xs, xt, ot = x.shape, x.stride(), out.stride()
+    if len(xs) != 3 or xs != out.shape or xs[0] != n or xs[2] != d or (
+            d > 1 and (xt[2] != 1 or ot[2] != 1)):
+        _bad(f"{what}: tensors are [n, heads, head_dim] with contiguous heads")
+    dx, do = _ROPE_DTYPES.get(x.dtype), _ROPE_DTYPES.get(out.dtype)
+    if dx is None or do is None:
+        _bad(f"{what}: bf16 or fp32")
+    return _ROPE_IO.pack(x.data_ptr(), out.data_ptr(), xt[0], xt[1], ot[0], ot[1], xs[1], dx, do)
 
 
 def _rope(what: str, fn, plan: Rope, pos, q, q_out, k, k_out, stream):
-    if pos.dim() == 1:
-        pos = pos.unsqueeze(0)
-    n = q.shape[0]
-    _want(pos.dtype == torch.int32 and pos.shape[0] >= plan.n_axes and pos.shape[1] == n
-          and (n <= 1 or pos.stride(1) == 1), f"{what}: pos is int32 [n_axes, n]")
-    _want((k is None) == (k_out is None), f"{what}: k and k_out come together")
-    st = _on(what, stream, plan.freq, pos, q, q_out, k, k_out)
+    n, ps, pt = q.shape[0], pos.shape, pos.stride()
+    if len(ps) == 1:
+        ps, pt = (1, ps[0]), (ps[0], pt[0])
+    if pos.dtype != torch.int32 or len(ps) != 2 or ps[0] < plan.n_axes or ps[1] != n or (
+            n > 1 and pt[1] != 1):
+        _bad(f"{what}: pos is int32 [n_axes, n]")
+    if (k is None) != (k_out is None):
+        _bad(f"{what}: k and k_out come together")
+    st = _on(what, stream, plan.dev, pos, q, q_out, k, k_out)
+    io, kio = _rope_io(what, n, plan.head_dim, q, q_out), None
     if k is not None:
-        _want(k.dtype == q.dtype and k_out.dtype == q_out.dtype, f"{what}: q and k have one dtype")
-    io = _rope_io(what, n, plan.head_dim, q, q_out)
-    kio = None if k is None else ctypes.byref(_rope_io(what, n, plan.head_dim, k, k_out))
-    stride = pos.stride(0) if pos.shape[0] > 1 else n
-    _ok(fn(ctypes.byref(plan._c), pos.data_ptr(), stride, n, ctypes.byref(io), kio, st), what)
+        if k.dtype != q.dtype or k_out.dtype != q_out.dtype:
+            _bad(f"{what}: q and k have one dtype")
+        kio = _rope_io(what, n, plan.head_dim, k, k_out)
+    code = fn(plan._r, pos.data_ptr(), pt[0] if ps[0] > 1 else n, n, io, kio, st)
+    if code:
+        _ok(code, what)
 
 
 def rope(plan: Rope, pos, q, q_out, k=None, k_out=None, stream=None):
@@ -876,6 +905,7 @@ class PagePool:
         self.work = torch.zeros(words, dtype=torch.int32, device=data.device)
         self._c.work = self.work.data_ptr()
         self._r = ctypes.byref(self._c)
+        self.dev = data.get_device()
 
     @staticmethod
     def allocate(n_planes: int, n_pages: int, page_bytes: int, page_tokens: int, n_rows: int,
@@ -892,46 +922,54 @@ class PagePool:
 def _list(what: str, *lists):
     n = lists[0].numel()
     for x in lists:
-        _want(x.dtype == torch.int32 and x.dim() == 1 and x.is_contiguous() and x.numel() == n,
-              f"{what}: lists are int32 vectors of one length")
+        if x.dtype != torch.int32 or x.dim() != 1 or x.numel() != n or not x.is_contiguous():
+            _bad(f"{what}: lists are int32 vectors of one length")
     return n
 
 
 def pages_reserve(pool: PagePool, rows, new_len, stream=None):
     """Row rows[i] grows to new_len[i] tokens (lowest free pages first)."""
     n = _list("hga_pages_reserve", rows, new_len)
-    st = _on("hga_pages_reserve", stream, pool.data, rows, new_len)
-    _ok(LIB.hga_pages_reserve(pool._r, rows.data_ptr(), new_len.data_ptr(), n, st),
-        "hga_pages_reserve")
+    st = _on("hga_pages_reserve", stream, pool.dev, rows, new_len)
+    code = LIB.hga_pages_reserve(pool._r, rows.data_ptr(), new_len.data_ptr(), n, st)
+    if code:
+        _ok(code, "hga_pages_reserve")
 
 
 def pages_fork(pool: PagePool, parents, children, stream=None):
     """Empty rows children[i] become copies of rows parents[i]: whole pages are
     shared, a last page that ends inside is copied."""
     n = _list("hga_pages_fork", parents, children)
-    st = _on("hga_pages_fork", stream, pool.data, parents, children)
-    _ok(LIB.hga_pages_fork(pool._r, parents.data_ptr(), children.data_ptr(), n, st),
-        "hga_pages_fork")
+    st = _on("hga_pages_fork", stream, pool.dev, parents, children)
+    code = LIB.hga_pages_fork(pool._r, parents.data_ptr(), children.data_ptr(), n, st)
+    if code:
+        _ok(code, "hga_pages_fork")
 
 
 def pages_free(pool: PagePool, rows, stream=None):
     """Returns the rows' pages and empties the rows."""
     n = _list("hga_pages_free", rows)
-    st = _on("hga_pages_free", stream, pool.data, rows)
-    _ok(LIB.hga_pages_free(pool._r, rows.data_ptr(), n, st), "hga_pages_free")
+    st = _on("hga_pages_free", stream, pool.dev, rows)
+    code = LIB.hga_pages_free(pool._r, rows.data_ptr(), n, st)
+    if code:
+        _ok(code, "hga_pages_free")
 
 
 def pages_compact(pool: PagePool, stream=None):
     """Moves the used pages to the front of the pool."""
-    st = _on("hga_pages_compact", stream, pool.data)
-    _ok(LIB.hga_pages_compact(pool._r, st), "hga_pages_compact")
+    st = _on("hga_pages_compact", stream, pool.dev)
+    code = LIB.hga_pages_compact(pool._r, st)
+    if code:
+        _ok(code, "hga_pages_compact")
 
 
 def pages_copy(pool: PagePool, src, dst, stream=None):
     """Copies pages src[i] to dst[i] in every plane."""
     n = _list("hga_pages_copy", src, dst)
-    st = _on("hga_pages_copy", stream, pool.data, src, dst)
-    _ok(LIB.hga_pages_copy(pool._r, src.data_ptr(), dst.data_ptr(), n, st), "hga_pages_copy")
+    st = _on("hga_pages_copy", stream, pool.dev, src, dst)
+    code = LIB.hga_pages_copy(pool._r, src.data_ptr(), dst.data_ptr(), n, st)
+    if code:
+        _ok(code, "hga_pages_copy")
 
 
 # ---------------------------------------------------------------- 4-bit K/V cache
@@ -947,6 +985,8 @@ class Q4Batch:
             _list("Q4Batch", off)
             _want(off.numel() == rows.numel() + 1, "Q4Batch: off is [n_seq + 1]")
         self.rows, self.off, self.max_q = rows, off, max_q
+        self.dev = rows.get_device()
+        _want(off is None or off.device == rows.device, "Q4Batch: rows and off are on one device")
         self._c = CQ4Batch(rows.data_ptr(), None if off is None else off.data_ptr(), rows.numel(),
                            max_q)
         self._r = ctypes.byref(self._c)
@@ -959,32 +999,34 @@ def q4_page_bytes(p: Params, page_tokens: int) -> int:
     return n
 
 
-def _q4_kv(what: str, p: Params, n: int, k, v, v_dtype):
-    shape = (n, p.n_kv_heads, p.head_dim)
-    _want(k.shape == shape and v.shape == shape and k.stride(2) == 1 and v.stride(2) == 1,
-          f"{what}: k and v are [n_tok, n_kv_heads, head_dim] with contiguous heads")
-    _want(k.dtype == p.torch_dtype and v.dtype == v_dtype, f"{what}: dtype")
+def _q4_kv(what: str, fn, p: Params, pool: PagePool, plane: int, batch: Q4Batch, k, v, v_dtype,
+           stream):
+    shape, kt, vt = k.shape, k.stride(), v.stride()
+    if len(shape) != 3 or shape[1] != p.n_kv_heads or shape[2] != p.head_dim or v.shape != shape or \
+            kt[2] != 1 or vt[2] != 1:
+        _bad(f"{what}: k and v are [n_tok, n_kv_heads, head_dim] with contiguous heads")
+    if k.dtype != p.torch_dtype or v.dtype != v_dtype:
+        _bad(f"{what}: dtype")
+    if batch.dev != pool.dev:
+        _bad(f"{what}: tensors must be on the current CUDA device")
+    st = _on(what, stream, pool.dev, k, v)
+    code = fn(_cp(p), pool._r, plane, batch._r, shape[0], k.data_ptr(), kt[0], kt[1], v.data_ptr(),
+              vt[0], vt[1], st)
+    if code:
+        _ok(code, what)
 
 
 def q4_append(p: Params, pool: PagePool, plane: int, batch: Q4Batch, k, v, stream=None):
     """Stores the batch's tokens: k, v [n_tok, Hkv, d] (any token and head
     strides), the last tokens of their rows (grow them with pages_reserve)."""
-    n = k.shape[0]
-    _q4_kv("hga_q4_append", p, n, k, v, p.torch_dtype)
-    st = _on("hga_q4_append", stream, pool.data, batch.rows, k, v)
-    _ok(LIB.hga_q4_append(_cp(p), pool._r, plane, batch._r, n, k.data_ptr(), k.stride(0),
-                          k.stride(1), v.data_ptr(), v.stride(0), v.stride(1), st),
-        "hga_q4_append")
+    _q4_kv("hga_q4_append", LIB.hga_q4_append, p, pool, plane, batch, k, v, p.torch_dtype, stream)
 
 
 def q4_read(p: Params, pool: PagePool, plane: int, batch: Q4Batch, k, v, stream=None):
     """Reads the batch's tokens back into k and v [n_tok, Hkv, d] (any strides,
     such as a [Hkv, t_cap, d] buffer's; v in fp16 with p.v_f16)."""
-    n = k.shape[0]
-    _q4_kv("hga_q4_read", p, n, k, v, torch.float16 if p.v_f16 else p.torch_dtype)
-    st = _on("hga_q4_read", stream, pool.data, batch.rows, k, v)
-    _ok(LIB.hga_q4_read(_cp(p), pool._r, plane, batch._r, n, k.data_ptr(), k.stride(0),
-                        k.stride(1), v.data_ptr(), v.stride(0), v.stride(1), st), "hga_q4_read")
+    _q4_kv("hga_q4_read", LIB.hga_q4_read, p, pool, plane, batch, k, v,
+           torch.float16 if p.v_f16 else p.torch_dtype, stream)
 
 
 def _work(n_bytes: int, device, stream):
@@ -1009,11 +1051,15 @@ def q4_routed_workspace(p: Params, n_q: int, device="cuda") -> Optional[torch.Te
 
 
 def _q4_out(what: str, p: Params, q, o, lse):
-    _want(q.dim() == 3 and q.shape[1] == p.n_q_heads and q.shape[2] == p.head_dim
-          and q.dtype == p.torch_dtype and q.is_contiguous() and o.shape == q.shape
-          and o.dtype == q.dtype and o.is_contiguous(), f"{what}: q and o are [n, Hq, d]")
-    _want(lse is None or (lse.dtype == torch.float32 and lse.shape == q.shape[:2]
-                          and lse.is_contiguous()), f"{what}: lse is float32 [n, Hq]")
+    shape = q.shape
+    if len(shape) != 3 or shape[1] != p.n_q_heads or shape[2] != p.head_dim or o.shape != shape or \
+            q.dtype != p.torch_dtype or o.dtype != q.dtype or not q.is_contiguous() or \
+            not o.is_contiguous():
+        _bad(f"{what}: q and o are [n, Hq, d]")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != shape[:2]
+                            or not lse.is_contiguous()):
+        _bad(f"{what}: lse is float32 [n, Hq]")
+    return shape[0]
 
 
 def q4_attend(p: Params, pool: PagePool, plane: int, batch: Q4Batch, q, o, lse=None,
@@ -1021,19 +1067,21 @@ def q4_attend(p: Params, pool: PagePool, plane: int, batch: Q4Batch, q, o, lse=N
     """Dense causal attention of the batch's tokens q [n_tok, Hq, d] over their
     rows' tokens.  max_ctx bounds the rows' lengths (default: the table's
     capacity); work: q4_workspace(...) of the caller (default: allocated here)."""
-    n = q.shape[0]
-    _q4_out("hga_q4_attend", p, q, o, lse)
-    st = _on("hga_q4_attend", stream, pool.data, batch.rows, q, o, lse, work)
+    n = _q4_out("hga_q4_attend", p, q, o, lse)
+    if batch.dev != pool.dev:
+        _bad("hga_q4_attend: tensors must be on the current CUDA device")
+    st = _on("hga_q4_attend", stream, pool.dev, q, o, lse, work)
     if max_ctx is None:
         max_ctx = pool.table.shape[1] * pool.page_tokens
     if work is None:
         need = LIB.hga_q4_attend_work(_cp(p), batch.rows.numel(), batch.max_q, n, max_ctx)
         work = _work(need, q.device, stream) if need > 0 else None
-    _ok(LIB.hga_q4_attend(_cp(p), pool._r, plane, batch._r, n, q.data_ptr(), max_ctx,
-                          o.data_ptr(), None if lse is None else lse.data_ptr(),
-                          None if work is None else work.data_ptr(),
-                          0 if work is None else work.numel() * work.element_size(), st),
-        "hga_q4_attend")
+    code = LIB.hga_q4_attend(_cp(p), pool._r, plane, batch._r, n, q.data_ptr(), max_ctx, o.data_ptr(),
+                             None if lse is None else lse.data_ptr(),
+                             None if work is None else work.data_ptr(),
+                             0 if work is None else work.nbytes, st)
+    if code:
+        _ok(code, "hga_q4_attend")
 
 
 def q4_attend_routed(p: Params, pool: PagePool, plane: int, row: int, q, q_start: int, t_cap: int,
@@ -1041,20 +1089,19 @@ def q4_attend_routed(p: Params, pool: PagePool, plane: int, row: int, q, q_start
                      stream=None):
     """attend with K and V in table row `row` of the pool.  pos_lo: rows of
     earlier positions are left as they are (default q_start: none)."""
-    n = q.shape[0]
-    _q4_out("hga_q4_attend_routed", p, q, o, lse)
+    n = _q4_out("hga_q4_attend_routed", p, q, o, lse)
     nb = (n + p.qblock - 1) // p.qblock
     _want(group_idx.dtype == torch.int32 and group_cnt.dtype == torch.int32
           and group_idx.is_contiguous() and group_cnt.is_contiguous()
           and group_cnt.shape == (p.n_kv_heads, nb)
           and group_idx.shape == (p.n_kv_heads, nb, max(index_capacity(p, t_cap, 1), 1)),
           "hga_q4_attend_routed: group_idx and group_cnt as allocate(p, t_cap, n_q) makes them")
-    st = _on("hga_q4_attend_routed", stream, pool.data, q, o, lse, group_idx, group_cnt, work)
+    st = _on("hga_q4_attend_routed", stream, pool.dev, q, o, lse, group_idx, group_cnt, work)
     if work is None:
         work = _work(LIB.hga_q4_attend_routed_work(_cp(p), n), q.device, stream)
     _ok(LIB.hga_q4_attend_routed(_cp(p), pool._r, plane, row, q.data_ptr(), q_start, n,
                                  q_start if pos_lo is None else pos_lo, t_cap,
                                  group_idx.data_ptr(), group_cnt.data_ptr(), o.data_ptr(),
                                  None if lse is None else lse.data_ptr(), work.data_ptr(),
-                                 work.numel() * work.element_size(), st),
+                                 work.nbytes, st),
         "hga_q4_attend_routed")
