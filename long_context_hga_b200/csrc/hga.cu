@@ -1165,9 +1165,11 @@ hga_status pool_args(const hga_page_pool* p, hga::PoolArgs* a) {
 }
 
 // Blocks of a page copy whose size only the device may know.
+int64_t copy_turns(const hga::PoolArgs& a, int64_t n) {
+  return (a.page_bytes / 16 + 4 * hga::kCopyThreads - 1) / (4 * hga::kCopyThreads) * a.n_planes * n;
+}
 unsigned copy_grid(const hga::PoolArgs& a, int64_t n) {
-  const int64_t pieces = (a.page_bytes / 16 + 4 * hga::kCopyThreads - 1) / (4 * hga::kCopyThreads);
-  const int64_t total = std::max<int64_t>(1, pieces * a.n_planes * n);
+  const int64_t total = std::max<int64_t>(1, copy_turns(a, n));
   return (unsigned)std::min<int64_t>(std::max<int64_t>(total, n), 148 * 8);
 }
 
@@ -1384,8 +1386,13 @@ hga_status hga_pages_fork(const hga_page_pool* pool, const int32_t* parents,
   if ((s = launch_pdl(hga::pages_fork_plan_kernel, dim3(1), dim3(hga::kPlanThreads), 0, st, a,
                       parents, children, n)) != HGA_OK)
     return s;
-  return launch_pdl(hga::pages_fork_kernel, dim3(copy_grid(a, n)), dim3(hga::kCopyThreads), 0, st,
-                    a, parents, children, n);
+  // four copies a turn where that still leaves every SM several turns
+  const unsigned grid = copy_grid(a, n);
+  return copy_turns(a, n) >= 148 * 8 * 4
+             ? launch_pdl(hga::pages_fork_kernel<4>, dim3(grid), dim3(hga::kCopyThreads), 0, st, a,
+                          parents, children, n)
+             : launch_pdl(hga::pages_fork_kernel<1>, dim3(grid), dim3(hga::kCopyThreads), 0, st, a,
+                          parents, children, n);
 }
 
 hga_status hga_pages_free(const hga_page_pool* pool, const int32_t* rows, int32_t n,

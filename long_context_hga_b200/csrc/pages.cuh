@@ -226,37 +226,46 @@ __global__ void __launch_bounds__(kPlanThreads) pages_fork_plan_kernel(PoolArgs 
   griddep_launch();
 }
 
-// Copies of whole pages over every plane.  Copy j (j < the count on the
-// device) moves page src[j] to dst[j]; pairs with a negative entry are
-// skipped.  The bytes of all copies are one long range of 16-byte vectors that
-// the grid strides over, four vectors of a thread in flight.
+// Copies of whole pages over every plane.  Copy j (j < n) moves page src[j] to
+// dst[j]; pairs with a negative entry are skipped.  A block's turn is 16 KB of a
+// page (four 16-byte vectors of a thread in flight) of GROUP neighbouring
+// copies: those from one source (a parent's children) read it once.
+template <int GROUP>
 __device__ __forceinline__ void copy_pages(const PoolArgs& a, const int32_t* src,
                                            const int32_t* dst, int n, int64_t block,
                                            int64_t n_blocks) {
   const int64_t vecs = a.page_bytes / 16;
   constexpr int kPiece = kCopyThreads * 4;
   const int64_t pieces = (vecs + kPiece - 1) / kPiece;
-  const int64_t total = pieces * a.n_planes * n;
+  const int groups = (n + GROUP - 1) / GROUP;
+  const int64_t total = pieces * a.n_planes * groups;
   for (int64_t w = block; w < total; w += n_blocks) {
     const int64_t pp = w / pieces, piece = w - pp * pieces;
-    const int plane = (int)(pp / n), j = (int)(pp - (int64_t)plane * n);
-    const int s = src[j], d = dst[j];
-    if (s < 0 || d < 0) continue;
-    const uint4* from = reinterpret_cast<const uint4*>(a.data + plane * a.plane_stride +
-                                                       s * a.page_bytes);
-    uint4* to = reinterpret_cast<uint4*>(a.data + plane * a.plane_stride + d * a.page_bytes);
-    uint4 v[4];
+    const int plane = (int)(pp / groups), j0 = (int)(pp - (int64_t)plane * groups) * GROUP;
+    char* base = a.data + plane * a.plane_stride;
     const int64_t at = piece * kPiece + threadIdx.x;
+    uint4 v[4];
+    int have = -1;
+    for (int j = j0; j < j0 + GROUP && j < n; ++j) {
+      const int s = src[j], d = dst[j];
+      if (s < 0 || d < 0) continue;
+      if (s != have) {
+        const uint4* from = reinterpret_cast<const uint4*>(base + s * a.page_bytes);
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (at + k * kCopyThreads < vecs) v[k] = from[at + k * kCopyThreads];
+        for (int k = 0; k < 4; ++k)
+          if (at + k * kCopyThreads < vecs) v[k] = from[at + k * kCopyThreads];
+        have = s;
+      }
+      uint4* to = reinterpret_cast<uint4*>(base + d * a.page_bytes);
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (at + k * kCopyThreads < vecs) __stcs(to + at + k * kCopyThreads, v[k]);
+      for (int k = 0; k < 4; ++k)
+        if (at + k * kCopyThreads < vecs) __stcs(to + at + k * kCopyThreads, v[k]);
+    }
   }
 }
 
 // Shares and copies of a planned fork: block i < n fills child i's table row.
+template <int GROUP>
 __global__ void __launch_bounds__(kCopyThreads) pages_fork_kernel(PoolArgs a,
                                                                   const int32_t* parents,
                                                                   const int32_t* children, int n) {
@@ -284,7 +293,7 @@ __global__ void __launch_bounds__(kCopyThreads) pages_fork_kernel(PoolArgs a,
     }
     if (threadIdx.x == 0) a.len[c] = len;
   }
-  copy_pages(a, a.wb, a.wc, n, blockIdx.x, gridDim.x);
+  copy_pages<GROUP>(a, a.wb, a.wc, n, blockIdx.x, gridDim.x);
 }
 
 // ---------------------------------------------------------------- compact
@@ -335,7 +344,7 @@ __global__ void __launch_bounds__(kCopyThreads) pages_compact_kernel(PoolArgs a)
     if (to >= 0) a.table[i] = to;
     else report(HGA_ERR_DEVICE_CHECK);    // no page of the pool, or a free one
   }
-  copy_pages(a, a.wa, a.wb, moves, blockIdx.x, gridDim.x);
+  copy_pages<1>(a, a.wa, a.wb, moves, blockIdx.x, gridDim.x);
 }
 
 // ---------------------------------------------------------------- copy
@@ -369,7 +378,7 @@ __global__ void __launch_bounds__(kPlanThreads) pages_copy_plan_kernel(PoolArgs 
 
 __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(PoolArgs a, int n) {
   griddep_wait();
-  copy_pages(a, a.wb, a.wc, n, blockIdx.x, gridDim.x);
+  copy_pages<1>(a, a.wb, a.wc, n, blockIdx.x, gridDim.x);
 }
 
 }  // namespace hga

@@ -18,6 +18,7 @@
 #pragma once
 #include <cuda_fp16.h>
 #include "common.cuh"
+#include "tc.cuh"
 
 namespace hga {
 
@@ -98,15 +99,18 @@ __device__ __forceinline__ float q4_scale(int b) {
   return __half2float(__ushort_as_half((unsigned short)(b << 7)));
 }
 
-// Smallest scale byte with 6 scale >= m (m >= 0, finite).
+// Smallest scale byte with 6 scale >= m, m in [0, 61440].  A byte is a half's
+// upper bits, so it is m / 6 rounded up, twice.  bf16: m has 8 bits, so m / 6 is a
+// scale's value or at least 2^-10 of itself away from one, and the product may
+// be too small by 2^-20 (checked for every m).  fp32: the guess is compared.
+template <typename T>
 __device__ __forceinline__ int q4_scale_byte(float m) {
-  m = fminf(m, kQ4MaxValue);
-  // a first guess from m / 6 rounded up to 4 significant bits, then exact
-  // comparisons (6 scale has 5 significant bits)
-  int b = (__half_as_ushort(__float2half_ru(m * 0.16666667f)) + 127) >> 7;
-  b = min(b, kQ4MaxScale);
-  while (b > 0 && 6.0f * q4_scale(b - 1) >= m) --b;
-  while (b < kQ4MaxScale && 6.0f * q4_scale(b) < m) ++b;
+  constexpr float kSixth = sizeof(T) == 2 ? 0.16666667f * (1.f - 0x1p-20f) : 0.16666667f;
+  int b = min((__half_as_ushort(__float2half_ru(m * kSixth)) + 127) >> 7, kQ4MaxScale);
+  if constexpr (sizeof(T) == 4) {
+    while (b > 0 && 6.0f * q4_scale(b - 1) >= m) --b;
+    while (b < kQ4MaxScale && 6.0f * q4_scale(b) < m) ++b;
+  }
   return b;
 }
 
@@ -120,43 +124,71 @@ __device__ __forceinline__ uint32_t q4_code2(float lo, float hi) {
   return r;
 }
 
-// x / s, exact where the quotient is a tie of the code grid.  For fp32 inputs a
-// correctly rounded quotient is enough: x has 24 bits and s 4, so a quotient
-// that is no tie lies more than half an ulp of the tie away from it.  bf16
-// inputs go through a product with 1/s, whose error (2^-23) is taken off by
-// rounding to a multiple of 2^-12: |x / s - tie| is 0 or at least 2^-10.
+// Eight values (half of a scale's 16; the thread beside has the others, lane
+// ^ 1) -> four code bytes and the scale byte.
+//
+// The maximum is taken over the magnitudes' bits, where infinities and NaN come
+// last.  x / s has to be exact where it is a tie of the code grid.  fp32: a
+// correctly rounded quotient is enough, x has 24 bits and s 4, so a quotient
+// that is no tie lies more than half an ulp of the tie away from it.  bf16: a
+// product with 1/s, whose error (2^-23) is taken off by rounding to a multiple
+// of 2^-12: |x / s - tie| is 0 or at least 2^-10.
 template <typename T>
-__device__ __forceinline__ float q4_ratio(float x, float s, float inv) {
-  if constexpr (sizeof(T) == 4) return __fdiv_rn(x, s);
-  return (x * inv + 2048.0f) - 2048.0f;
-}
-
-// 16 values -> 8 code bytes and the scale byte.
-template <typename T>
-__device__ __forceinline__ uint2 q4_encode(const float* f, int* scale, bool* bad) {
-  float m = 0.f;
-  bool over = false;
+__device__ __forceinline__ uint32_t q4_encode8(const T* src, int lane, int* scale, bool* bad) {
+  float f[8];
+  uint32_t top = 0;
+  if constexpr (sizeof(T) == 2) {
+    const uint4 raw = *reinterpret_cast<const uint4*>(src);
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    m = fmaxf(m, fabsf(f[i]));
-    over |= !(fabsf(f[i]) <= kQ4MaxValue);     // NaN too
-  }
-  *bad |= over;
-  const int b = q4_scale_byte(m);
-  *scale = b;
-  if (b == 0) return make_uint2(0, 0);
-  const float s = q4_scale(b), inv = 1.0f / s;
-  uint32_t w[2] = {0, 0};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float x = f[2 * i], y = f[2 * i + 1];
-    if (over) {
-      x = x == x ? fminf(fmaxf(x, -kQ4MaxValue), kQ4MaxValue) : 0.f;
-      y = y == y ? fminf(fmaxf(y, -kQ4MaxValue), kQ4MaxValue) : 0.f;
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      top = __vmaxu2(top, w[i] & 0x7fff7fffu);
     }
-    w[i >> 2] |= q4_code2(q4_ratio<T>(x, s, inv), q4_ratio<T>(y, s, inv)) << (8 * (i & 3));
+    top = max(top << 16, top & 0xffff0000u);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float4 r = reinterpret_cast<const float4*>(src)[i];
+      f[4 * i] = r.x; f[4 * i + 1] = r.y; f[4 * i + 2] = r.z; f[4 * i + 3] = r.w;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(f[i]) & 0x7fffffffu);
   }
-  return make_uint2(w[0], w[1]);
+  const unsigned both = 3u << (lane & 30);
+  top = max(top, __shfl_xor_sync(both, top, 1));
+  float m = __uint_as_float(top);
+  if (!(m <= kQ4MaxValue)) {
+    *bad = true;
+    m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      f[i] = f[i] == f[i] ? fminf(fmaxf(f[i], -kQ4MaxValue), kQ4MaxValue) : 0.f;
+      m = fmaxf(m, fabsf(f[i]));
+    }
+    m = fmaxf(m, __shfl_xor_sync(both, m, 1));
+  }
+  const int b = q4_scale_byte<T>(m);
+  *scale = b;
+  if (b == 0) return 0;
+  const float s = q4_scale(b);
+  uint32_t code = 0;
+  if constexpr (sizeof(T) == 2) {
+    const float inv = 1.0f / s;
+    const uint64_t inv2 = tc::pk2(inv, inv), up = tc::pk2(2048.f, 2048.f), down = tc::pk2(-2048.f, -2048.f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float x, y;
+      tc::unpk2(tc::fadd2(tc::ffma2(tc::pk2(f[2 * i], f[2 * i + 1]), inv2, up), down), x, y);
+      code |= q4_code2(x, y) << (8 * i);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      code |= q4_code2(__fdiv_rn(f[2 * i], s), __fdiv_rn(f[2 * i + 1], s)) << (8 * i);
+  }
+  return code;
 }
 
 // Eight codes (one word) -> four pairs of fp16.
@@ -226,9 +258,9 @@ __device__ __forceinline__ void q4_block_tokens(const Q4IoArgs& a, int64_t t0, i
   __syncthreads();
 }
 
-// One thread per 16 values of K and the same 16 of V: the maximum needs no
-// exchange between threads.  Bound: HBM (reads 4 d, writes 9 d / 8 bytes per
-// token and head).
+// One thread per 8 values of K and the same 8 of V, so that a warp's 16-byte
+// loads are contiguous; the two threads of a scale exchange their maxima.
+// Bound: HBM (reads 4 d, writes 9 d / 8 bytes per token and head).
 template <typename T>
 __global__ void __launch_bounds__(kQ4Threads) q4_append_kernel(const Q4IoArgs a) {
   __shared__ Q4BlockTokens tok;
@@ -236,8 +268,9 @@ __global__ void __launch_bounds__(kQ4Threads) q4_append_kernel(const Q4IoArgs a)
   const int64_t t0 = (int64_t)blockIdx.x * a.toks;
   const int nt = (int)min((int64_t)a.toks, a.n_tok - t0);
   q4_block_tokens(a, t0, nt, &tok);
-  const int nb = a.D >> 4, log_nb = a.D == 128 ? 3 : 2;   // scale blocks of a head's row
-  const int hb = a.c.Hkv << log_nb;
+  const int lane = threadIdx.x & 31;
+  const int half = a.D >> 1, log_nv = a.D == 128 ? 4 : 3, nb = a.D >> 4;
+  const int hb = a.c.Hkv << log_nv;                 // threads of a token
   bool bad = false;
   // a row named by two sequences of the call would be written twice: reported
   for (int i = blockIdx.x * kQ4Threads + threadIdx.x; i < a.b.n_seq; i += gridDim.x * kQ4Threads)
@@ -247,19 +280,19 @@ __global__ void __launch_bounds__(kQ4Threads) q4_append_kernel(const Q4IoArgs a)
   int t = threadIdx.x / hb, x = threadIdx.x % hb;
   for (; t < nt; t += dt + (x + dx >= hb), x = x + dx >= hb ? x + dx - hb : x + dx) {
     if (tok.off[t] < 0) continue;
-    const int h = x >> log_nb, blk = x & (nb - 1), r = tok.r[t];
+    const int h = x >> log_nv, v8 = x & ((1 << log_nv) - 1), r = tok.r[t];
     char* rec = a.c.base + tok.off[t] + (int64_t)h * a.c.page_recs * q4_record_bytes(a.D);
-    float k[16], v[16];
-    q4_load16(static_cast<const T*>(a.k) + (t0 + t) * a.k_tok + h * a.k_head + blk * 16, k);
-    q4_load16(static_cast<const T*>(a.v) + (t0 + t) * a.v_tok + h * a.v_head + blk * 16, v);
     int ks, vs;
-    const uint2 kc = q4_encode<T>(k, &ks, &bad);
-    const uint2 vc = q4_encode<T>(v, &vs, &bad);
-    const int half = a.D >> 1;
-    *reinterpret_cast<uint2*>(rec + r * half + blk * 8) = kc;
-    *reinterpret_cast<uint2*>(rec + 8 * half + r * half + blk * 8) = vc;
-    rec[16 * half + r * nb + blk] = (char)ks;
-    rec[16 * half + 8 * nb + r * nb + blk] = (char)vs;
+    const uint32_t kc = q4_encode8(
+        static_cast<const T*>(a.k) + (t0 + t) * a.k_tok + h * a.k_head + v8 * 8, lane, &ks, &bad);
+    const uint32_t vc = q4_encode8(
+        static_cast<const T*>(a.v) + (t0 + t) * a.v_tok + h * a.v_head + v8 * 8, lane, &vs, &bad);
+    *reinterpret_cast<uint32_t*>(rec + r * half + v8 * 4) = kc;
+    *reinterpret_cast<uint32_t*>(rec + 8 * half + r * half + v8 * 4) = vc;
+    // the even thread has K's scale, the odd one V's
+    const int sb = r * nb + (v8 >> 1);
+    if (v8 & 1) rec[16 * half + 8 * nb + sb] = (char)vs;
+    else rec[16 * half + sb] = (char)ks;
   }
   if (bad) report(HGA_ERR_DEVICE_CHECK);
   griddep_launch();
@@ -267,37 +300,33 @@ __global__ void __launch_bounds__(kQ4Threads) q4_append_kernel(const Q4IoArgs a)
 
 // ---------------------------------------------------------------- read
 
-// The batch's tokens back as the values their codes stand for, in TK and TV
-// (exact in bf16, fp16 and fp32).
+// 8 codes -> 16 bytes of fp16 or bf16 or 32 of fp32, exact.
 template <typename T>
-__device__ __forceinline__ void q4_decode16(const uint2 codes, int scale, T* out) {
-  const uint32_t s2 = (uint32_t)(scale << 7) * 0x10001u;
-  uint32_t h[8];
-  q4_unpack8(codes.x, h);
-  q4_unpack8(codes.y, h + 4);
+__device__ __forceinline__ void q4_decode8(uint32_t codes, int scale, T* out) {
+  const uint32_t s2 = (uint32_t)scale * 0x00800080u;
+  uint32_t h[4];
+  q4_unpack8(codes, h);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) h[i] = q4_mul2(h[i], s2);
-  if constexpr (sizeof(T) == 2) {
-    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float2 f = __half22float2(*reinterpret_cast<__half2*>(&h[i]));
-        const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
-        h[i] = *reinterpret_cast<const uint32_t*>(&b);
-      }
-    }
-    reinterpret_cast<uint4*>(out)[0] = make_uint4(h[0], h[1], h[2], h[3]);
-    reinterpret_cast<uint4*>(out)[1] = make_uint4(h[4], h[5], h[6], h[7]);
+  for (int i = 0; i < 4; ++i) h[i] = q4_mul2(h[i], s2);
+  if constexpr (std::is_same<T, __half>::value) {
+    *reinterpret_cast<uint4*>(out) = make_uint4(h[0], h[1], h[2], h[3]);
   } else {
+    float2 f[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = __half22float2(*reinterpret_cast<__half2*>(&h[2 * i]));
-      const float2 g = __half22float2(*reinterpret_cast<__half2*>(&h[2 * i + 1]));
-      reinterpret_cast<float4*>(out)[i] = make_float4(f.x, f.y, g.x, g.y);
+    for (int i = 0; i < 4; ++i) f[i] = __half22float2(*reinterpret_cast<__half2*>(&h[i]));
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) h[i] = tc::pack_bf162(f[i].x, f[i].y);
+      *reinterpret_cast<uint4*>(out) = make_uint4(h[0], h[1], h[2], h[3]);
+    } else {
+      reinterpret_cast<float4*>(out)[0] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+      reinterpret_cast<float4*>(out)[1] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
     }
   }
 }
 
+// The batch's tokens back as the values their codes stand for, in TK and TV.
+// One thread per 8 values of K and of V: contiguous 16-byte stores.
 template <typename TK, typename TV>
 __global__ void __launch_bounds__(kQ4Threads) q4_read_kernel(const Q4IoArgs a) {
   __shared__ Q4BlockTokens tok;
@@ -305,20 +334,21 @@ __global__ void __launch_bounds__(kQ4Threads) q4_read_kernel(const Q4IoArgs a) {
   const int64_t t0 = (int64_t)blockIdx.x * a.toks;
   const int nt = (int)min((int64_t)a.toks, a.n_tok - t0);
   q4_block_tokens(a, t0, nt, &tok);
-  const int nb = a.D >> 4, log_nb = a.D == 128 ? 3 : 2, half = a.D >> 1;
-  const int hb = a.c.Hkv << log_nb;
+  const int half = a.D >> 1, log_nv = a.D == 128 ? 4 : 3, nb = a.D >> 4;
+  const int hb = a.c.Hkv << log_nv;
   const int dt = kQ4Threads / hb, dx = kQ4Threads % hb;
   int t = threadIdx.x / hb, x = threadIdx.x % hb;
+#pragma unroll 2
   for (; t < nt; t += dt + (x + dx >= hb), x = x + dx >= hb ? x + dx - hb : x + dx) {
     if (tok.off[t] < 0) continue;
-    const int h = x >> log_nb, blk = x & (nb - 1), r = tok.r[t];
+    const int h = x >> log_nv, v8 = x & ((1 << log_nv) - 1), r = tok.r[t];
     const char* rec = a.c.base + tok.off[t] + (int64_t)h * a.c.page_recs * q4_record_bytes(a.D);
-    const uint2 kc = *reinterpret_cast<const uint2*>(rec + r * half + blk * 8);
-    const uint2 vc = *reinterpret_cast<const uint2*>(rec + 8 * half + r * half + blk * 8);
-    const int ks = (unsigned char)rec[16 * half + r * nb + blk];
-    const int vs = (unsigned char)rec[16 * half + 8 * nb + r * nb + blk];
-    q4_decode16(kc, ks, (TK*)a.k + (t0 + t) * a.k_tok + h * a.k_head + blk * 16);
-    q4_decode16(vc, vs, (TV*)a.v + (t0 + t) * a.v_tok + h * a.v_head + blk * 16);
+    const uint32_t kc = *reinterpret_cast<const uint32_t*>(rec + r * half + v8 * 4);
+    const uint32_t vc = *reinterpret_cast<const uint32_t*>(rec + 8 * half + r * half + v8 * 4);
+    const int sb = 16 * half + r * nb + (v8 >> 1);
+    const int ks = (unsigned char)rec[sb], vs = (unsigned char)rec[sb + 8 * nb];
+    q4_decode8(kc, ks, (TK*)a.k + (t0 + t) * a.k_tok + h * a.k_head + v8 * 8);
+    q4_decode8(vc, vs, (TV*)a.v + (t0 + t) * a.v_tok + h * a.v_head + v8 * 8);
   }
   griddep_launch();
 }
