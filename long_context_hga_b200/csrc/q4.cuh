@@ -114,31 +114,35 @@ __device__ __forceinline__ int q4_scale_byte(float m) {
   return b;
 }
 
-// Codes of two values already divided by their scale (first one in the low nibble).
-__device__ __forceinline__ uint32_t q4_code2(float lo, float hi) {
+// Codes of eight values already divided by their scale (the first one in the
+// low nibble).
+__device__ __forceinline__ uint32_t q4_code8(const float* f) {
   uint32_t r;
-  asm("{\n .reg .b8 c;\n cvt.rn.satfinite.e2m1x2.f32 c, %1, %2;\n"
-      " mov.b32 %0, {c, 0, 0, 0};\n}\n"
+  asm("{\n .reg .b8 a, b, c, d;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n"
+      " mov.b32 %0, {a, b, c, d};\n}\n"
       : "=r"(r)
-      : "f"(hi), "f"(lo));
+      : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]));
   return r;
 }
 
 // Eight values (half of a scale's 16; the thread beside has the others, lane
-// ^ 1) -> four code bytes and the scale byte.
+// ^ 1) -> four code bytes and the scale byte.  Called by whole warps; a thread
+// that is not live reads nothing.
 //
 // The maximum is taken over the magnitudes' bits, where infinities and NaN come
 // last.  x / s has to be exact where it is a tie of the code grid.  fp32: a
 // correctly rounded quotient is enough, x has 24 bits and s 4, so a quotient
 // that is no tie lies more than half an ulp of the tie away from it.  bf16: a
-// product with 1/s, whose error (2^-23) is taken off by rounding to a multiple
-// of 2^-12: |x / s - tie| is 0 or at least 2^-10.
+// product with 1/s (together good to 2^-21 of at most 7) whose error is taken off
+// by rounding to a multiple of 2^-12: |x / s - tie| is 0 or at least 2^-10.
 template <typename T>
-__device__ __forceinline__ uint32_t q4_encode8(const T* src, int lane, int* scale, bool* bad) {
+__device__ __forceinline__ uint32_t q4_encode8(const T* src, bool live, int* scale, bool* bad) {
   float f[8];
   uint32_t top = 0;
   if constexpr (sizeof(T) == 2) {
-    const uint4 raw = *reinterpret_cast<const uint4*>(src);
+    const uint4 raw = live ? *reinterpret_cast<const uint4*>(src) : make_uint4(0, 0, 0, 0);
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -150,45 +154,40 @@ __device__ __forceinline__ uint32_t q4_encode8(const T* src, int lane, int* scal
   } else {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float4 r = reinterpret_cast<const float4*>(src)[i];
+      const float4 r = live ? reinterpret_cast<const float4*>(src)[i] : make_float4(0.f, 0.f, 0.f, 0.f);
       f[4 * i] = r.x; f[4 * i + 1] = r.y; f[4 * i + 2] = r.z; f[4 * i + 3] = r.w;
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(f[i]) & 0x7fffffffu);
   }
-  const unsigned both = 3u << (lane & 30);
-  top = max(top, __shfl_xor_sync(both, top, 1));
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
   float m = __uint_as_float(top);
-  if (!(m <= kQ4MaxValue)) {
-    *bad = true;
+  const bool over = !(m <= kQ4MaxValue);
+  if (__any_sync(0xffffffffu, over)) {
+    *bad |= over;
     m = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       f[i] = f[i] == f[i] ? fminf(fmaxf(f[i], -kQ4MaxValue), kQ4MaxValue) : 0.f;
       m = fmaxf(m, fabsf(f[i]));
     }
-    m = fmaxf(m, __shfl_xor_sync(both, m, 1));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
   }
   const int b = q4_scale_byte<T>(m);
   *scale = b;
-  if (b == 0) return 0;
-  const float s = q4_scale(b);
-  uint32_t code = 0;
+  const float s = b == 0 ? 1.f : q4_scale(b);   // 0: every value is 0
   if constexpr (sizeof(T) == 2) {
-    const float inv = 1.0f / s;
+    const float inv = __fdividef(1.0f, s);
     const uint64_t inv2 = tc::pk2(inv, inv), up = tc::pk2(2048.f, 2048.f), down = tc::pk2(-2048.f, -2048.f);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float x, y;
-      tc::unpk2(tc::fadd2(tc::ffma2(tc::pk2(f[2 * i], f[2 * i + 1]), inv2, up), down), x, y);
-      code |= q4_code2(x, y) << (8 * i);
-    }
+    for (int i = 0; i < 4; ++i)
+      tc::unpk2(tc::fadd2(tc::ffma2(tc::pk2(f[2 * i], f[2 * i + 1]), inv2, up), down), f[2 * i],
+                f[2 * i + 1]);
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      code |= q4_code2(__fdiv_rn(f[2 * i], s), __fdiv_rn(f[2 * i + 1], s)) << (8 * i);
+    for (int i = 0; i < 8; ++i) f[i] = __fdiv_rn(f[i], s);
   }
-  return code;
+  return q4_code8(f);
 }
 
 // Eight codes (one word) -> four pairs of fp16.
@@ -268,7 +267,6 @@ __global__ void __launch_bounds__(kQ4Threads) q4_append_kernel(const Q4IoArgs a)
   const int64_t t0 = (int64_t)blockIdx.x * a.toks;
   const int nt = (int)min((int64_t)a.toks, a.n_tok - t0);
   q4_block_tokens(a, t0, nt, &tok);
-  const int lane = threadIdx.x & 31;
   const int half = a.D >> 1, log_nv = a.D == 128 ? 4 : 3, nb = a.D >> 4;
   const int hb = a.c.Hkv << log_nv;                 // threads of a token
   bool bad = false;
@@ -278,21 +276,27 @@ __global__ void __launch_bounds__(kQ4Threads) q4_append_kernel(const Q4IoArgs a)
       if (a.b.rows[i] >= 0 && a.b.rows[j] == a.b.rows[i]) bad = true;
   const int dt = kQ4Threads / hb, dx = kQ4Threads % hb;
   int t = threadIdx.x / hb, x = threadIdx.x % hb;
-  for (; t < nt; t += dt + (x + dx >= hb), x = x + dx >= hb ? x + dx - hb : x + dx) {
-    if (tok.off[t] < 0) continue;
-    const int h = x >> log_nv, v8 = x & ((1 << log_nv) - 1), r = tok.r[t];
-    char* rec = a.c.base + tok.off[t] + (int64_t)h * a.c.page_recs * q4_record_bytes(a.D);
+  const int turns = (nt * hb + kQ4Threads - 1) / kQ4Threads;   // whole warps: the maxima are exchanged
+  for (int i = 0; i < turns; ++i) {
+    const bool live = t < nt && tok.off[t] >= 0;
+    const int tt = live ? t : 0;
+    const int h = x >> log_nv, v8 = x & ((1 << log_nv) - 1), r = tok.r[tt];
+    char* rec = a.c.base + tok.off[tt] + (int64_t)h * a.c.page_recs * q4_record_bytes(a.D);
     int ks, vs;
     const uint32_t kc = q4_encode8(
-        static_cast<const T*>(a.k) + (t0 + t) * a.k_tok + h * a.k_head + v8 * 8, lane, &ks, &bad);
+        static_cast<const T*>(a.k) + (t0 + tt) * a.k_tok + h * a.k_head + v8 * 8, live, &ks, &bad);
     const uint32_t vc = q4_encode8(
-        static_cast<const T*>(a.v) + (t0 + t) * a.v_tok + h * a.v_head + v8 * 8, lane, &vs, &bad);
-    *reinterpret_cast<uint32_t*>(rec + r * half + v8 * 4) = kc;
-    *reinterpret_cast<uint32_t*>(rec + 8 * half + r * half + v8 * 4) = vc;
-    // the even thread has K's scale, the odd one V's
-    const int sb = r * nb + (v8 >> 1);
-    if (v8 & 1) rec[16 * half + 8 * nb + sb] = (char)vs;
-    else rec[16 * half + sb] = (char)ks;
+        static_cast<const T*>(a.v) + (t0 + tt) * a.v_tok + h * a.v_head + v8 * 8, live, &vs, &bad);
+    if (live) {
+      *reinterpret_cast<uint32_t*>(rec + r * half + v8 * 4) = kc;
+      *reinterpret_cast<uint32_t*>(rec + 8 * half + r * half + v8 * 4) = vc;
+      // the even thread has K's scale, the odd one V's
+      const int sb = r * nb + (v8 >> 1);
+      if (v8 & 1) rec[16 * half + 8 * nb + sb] = (char)vs;
+      else rec[16 * half + sb] = (char)ks;
+    }
+    t += dt + (x + dx >= hb);
+    x = x + dx >= hb ? x + dx - hb : x + dx;
   }
   if (bad) report(HGA_ERR_DEVICE_CHECK);
   griddep_launch();
