@@ -488,6 +488,8 @@ hga_status attend_impl(const hga_params* p, const void* q, int64_t q_start, int6
   a.q_early = p->q_ready;
   const int64_t max_list = p->sink / p->group + a.cap_g + p->local / p->group +
                            (p->qblock + p->group - 1) / p->group;
+  if (max_list > 16384) return HGA_ERR_UNSUPPORTED;
+  a.max_list = (int)max_list;
   a.scale_log2 = (float)(1.4426950408889634 / sqrt((double)p->head_dim));
   a.pos_lo = pos_lo;
   if (p->dtype == HGA_BF16 && p->v_f16)
@@ -618,6 +620,8 @@ hga_status hga_attend_backward(const hga_params* p, const void* q, int64_t q_sta
   a.local = p->local;
   const int64_t max_list = p->sink / p->group + a.cap_g + p->local / p->group +
                            (p->qblock + p->group - 1) / p->group;
+  if (max_list > 16384) return HGA_ERR_UNSUPPORTED;
+  a.max_list = (int)max_list;
   w.o = o;
   w.d_o = d_o;
   w.lse = lse;
