@@ -11,7 +11,7 @@
 //
 // Warp roles (512 threads, registers split 80 : 176):
 //   warp 0       TMEM owner and MMA issuer
-//   warp 1       fetches records, 8 at a time, into a ring by bulk copies
+//   warps 1-2    fetch records, 8 at a time by turns, into a ring by bulk copies
 //   warps 4-7    expand: convert codes into the 128-byte swizzled operand
 //                layout; tokens past the sequence and missing pages become zeros
 //   warps 8-15   softmax of Q0 and Q1, one thread per row (of every 16
@@ -41,6 +41,7 @@ constexpr int kQ4TcExpand = 128;           // threads that expand K and V
 constexpr int kQ4TcSlots = 2;              // expanded K (and V) steps in shared memory
 constexpr float kQ4TcShift = 7.f;
 
+// A warp arrives once, after every lane's fence.
 struct Q4TcBars {
   uint64_t q_full, k_full[kQ4TcSlots], k_empty[kQ4TcSlots], v_full[kQ4TcSlots],
       v_empty[kQ4TcSlots];
@@ -189,17 +190,17 @@ __global__ void __launch_bounds__(kQ4TcThreads, 1) q4_attend_tc_kernel(const Q4A
 
   if (tid == 0) {
     bars->abort = 0;
-    tc::mbar_init(&bars->q_full, nq * kTcRows);
+    tc::mbar_init(&bars->q_full, nq * 4);
     for (int s = 0; s < kQ4TcSlots; ++s) {
-      tc::mbar_init(&bars->k_full[s], kQ4TcExpand);
-      tc::mbar_init(&bars->v_full[s], kQ4TcExpand);
+      tc::mbar_init(&bars->k_full[s], kQ4TcExpand / 32);
+      tc::mbar_init(&bars->v_full[s], kQ4TcExpand / 32);
       tc::mbar_init(&bars->k_empty[s], 1);
       tc::mbar_init(&bars->v_empty[s], 1);
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&bars->s_full[i], 1);
       tc::mbar_init(&bars->o_full[i], 1);
-      for (int x = 0; x < 2; ++x) tc::mbar_init(&bars->p_full[i][x], kTcRows);
+      for (int x = 0; x < 2; ++x) tc::mbar_init(&bars->p_full[i][x], 4);
     }
     tc::mbar_init(&bars->done, 1);
     for (int s = 0; s < L::kStages; ++s) {
@@ -226,10 +227,10 @@ __global__ void __launch_bounds__(kQ4TcThreads, 1) q4_attend_tc_kernel(const Q4A
     if (warp == 0 && nt > 0) {
       // ---------------------------------------------------------- MMA issuer
       q4_tc_mma<D>(bars, tmem, tc::smem_addr(smem), nq, nt, abort_flag);
-    } else if (warp == 1) {
+    } else if (warp == 1 || warp == 2) {
       // ---------------------------------------------------------- fetch
       // Load n is half n % 2 (8 records) of step n / 2.  Lane e < 8 owns record
-      // e; the place of the next load's records is looked up one load ahead.
+      // e; the places of a warp's next load are looked up one load ahead.
       const int32_t* pages = g.c.table + (int64_t)max(u.row, 0) * g.c.row_pages;
       int last_use[L::kStages];
 #pragma unroll
@@ -240,10 +241,13 @@ __global__ void __launch_bounds__(kQ4TcThreads, 1) q4_attend_tc_kernel(const Q4A
         ent = lane < 8 && n < 2 * nt ? q4_entry<ROUTED>(list, t_lo * 16 + n * 8 + lane) : -1;
         at = ent >= 0 ? q4_where(g.c, pages, h, ent, q4_record_bytes(D)) : -1;
       };
-      look(0);
-      int s = 0, u_s = 0;
-      for (int n = 0; n < 2 * nt; ++n) {
-        if (n >= L::kStages && !tc::mbar_wait_warp(&bars->raw_empty[s], (u_s - 1) & 1, abort_flag)) break;
+      bool gave_up = false;
+      look(warp - 1);
+      for (int n = warp - 1; n < 2 * nt; n += 2) {
+        const int s = n % L::kStages, u_s = n / L::kStages;
+        if (n >= L::kStages &&
+            (gave_up = !tc::mbar_wait_warp(&bars->raw_empty[s], (u_s - 1) & 1, abort_flag)))
+          break;
         // entries of the load for the masks, eight loads (four steps) deep: the
         // slot was read by the softmax of step j - 4, which is done once the
         // first half of step j - 2 is expanded (that waits for the slots of
@@ -256,11 +260,11 @@ __global__ void __launch_bounds__(kQ4TcThreads, 1) q4_attend_tc_kernel(const Q4A
 #pragma unroll
         for (int x = 0; x < L::kStages; ++x)
           if (x == s) last_use[x] = u_s;
-        look(n + 1);
-        if (++s == L::kStages) s = 0, ++u_s;
+        look(n + 2);
       }
-      // no copy may still be landing when the block's memory goes
-      if (lane == 0) {
+      // no copy may still be landing when the block's memory goes: the expanding
+      // warps have waited for every one, unless the block gives up
+      if ((gave_up || *abort_flag) && lane == 0) {
 #pragma unroll
         for (int x = 0; x < L::kStages; ++x) {
           if (last_use[x] < 0) continue;
@@ -322,7 +326,8 @@ __global__ void __launch_bounds__(kQ4TcThreads, 1) q4_attend_tc_kernel(const Q4A
           }
           if (n & 1) {
             tc::fence_proxy_async_smem();
-            tc::mbar_arrive(v ? &bars->v_full[s] : &bars->k_full[s]);
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(v ? &bars->v_full[s] : &bars->k_full[s]);
           }
         }
         if (!ok) break;
@@ -343,36 +348,58 @@ __global__ void __launch_bounds__(kQ4TcThreads, 1) q4_attend_tc_kernel(const Q4A
     const uint32_t t_s = t_row + i * 128, t_o = t_row + 256 + i * 128;
     float sc = 1.f;                             // log2 units of a score
     if (i < nq && nt > 0) {
-      // q's row as fp16 relative to a power of two, in the operand layout
-      const uint4* src = reinterpret_cast<const uint4*>(
-          static_cast<const __nv_bfloat16*>(g.a.q) + orow * D);
-      uint4 raw[D / 8];
-      uint32_t top = 0;
+      // q's rows as fp16 relative to a power of two, in the operand layout: a
+      // warp brings its 32 rows in together, then each lane scales its own
+      constexpr int kLanes = D / 8, kAt = 32 / kLanes;    // lanes of a row, rows at a time
+      char* rows = smem + L::kQOff + i * L::kHalves * L::kHalfBytes;
+      auto chunk = [&](int rr, int x) {                   // 16 bytes of a row
+        return reinterpret_cast<uint4*>(rows + (x >> 3) * L::kHalfBytes + rr * 128 +
+                                        (((x & 7) ^ (rr & 7)) * 16));
+      };
+      const int x = lane % kLanes;
 #pragma unroll
-      for (int x = 0; x < D / 8; ++x) {
-        raw[x] = row_live ? src[x] : make_uint4(0, 0, 0, 0);
-        const uint32_t v[4] = {raw[x].x, raw[x].y, raw[x].z, raw[x].w};
+      for (int it0 = 0; it0 < kLanes; it0 += 8) {
+        uint4 raw[8];
 #pragma unroll
-        for (int y = 0; y < 4; ++y) top = max(top, max(v[y] & 0x7fffu, (v[y] >> 16) & 0x7fffu));
+        for (int it = 0; it < 8; ++it) {
+          const int rr = (it0 + it) * kAt + lane / kLanes;
+          const int64_t at = __shfl_sync(0xffffffffu, orow, rr);
+          raw[it] = make_uint4(0, 0, 0, 0);
+          if (unit_row - lane + rr < nrows)
+            raw[it] = *reinterpret_cast<const uint4*>(
+                static_cast<const __nv_bfloat16*>(g.a.q) + at * D + x * 8);
+        }
+#pragma unroll
+        for (int it = 0; it < 8; ++it)
+          *chunk(quarter * 32 + (it0 + it) * kAt + lane / kLanes, x) = raw[it];
       }
+      __syncwarp();
+      uint32_t top = 0;
+#pragma unroll 4
+      for (int y = 0; y < kLanes; ++y) {
+        const uint4 v = *chunk(r, y);
+        top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                                     __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+      }
+      top = max(top & 0xffffu, top >> 16);
       int ex = (int)(top >> 7);
       ex = top == 0 ? 127 : min(max(ex, 1), 253);
       const float down = __uint_as_float((uint32_t)(254 - ex) << 23);
       sc = __uint_as_float((uint32_t)ex << 23) * g.a.scale_log2;
-      char* row = smem + L::kQOff + i * L::kHalves * L::kHalfBytes + r * 128;
-#pragma unroll
-      for (int x = 0; x < D / 8; ++x) {
-        const uint32_t v[4] = {raw[x].x, raw[x].y, raw[x].z, raw[x].w};
+#pragma unroll 4
+      for (int y = 0; y < kLanes; ++y) {
+        const uint4 raw = *chunk(r, y);
+        const uint32_t v[4] = {raw.x, raw.y, raw.z, raw.w};
         uint32_t o[4];
 #pragma unroll
-        for (int y = 0; y < 4; ++y)
-          o[y] = tc::pack_half2(__uint_as_float(v[y] << 16) * down,
-                                __uint_as_float(v[y] & 0xffff0000u) * down);
-        *reinterpret_cast<uint4*>(row + (x >> 3) * L::kHalfBytes + (((x & 7) ^ (r & 7)) * 16)) =
-            make_uint4(o[0], o[1], o[2], o[3]);
+        for (int w = 0; w < 4; ++w)
+          o[w] = tc::pack_half2(__uint_as_float(v[w] << 16) * down,
+                                __uint_as_float(v[w] & 0xffff0000u) * down);
+        *chunk(r, y) = make_uint4(o[0], o[1], o[2], o[3]);
       }
       tc::fence_proxy_async_smem();
-      tc::mbar_arrive(&bars->q_full);
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&bars->q_full);
     }
     float m = -INFINITY, l = 0.f;               // m: a score, not scaled
     bool ok = i < nq;
@@ -460,7 +487,8 @@ __global__ void __launch_bounds__(kQ4TcThreads, 1) q4_attend_tc_kernel(const Q4A
         tc::tmem_st32(t_s + hf * 32, pk);
         tc::tmem_wait_st();
         tc::fence_before_sync();
-        tc::mbar_arrive(&bars->p_full[i][hf]);
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bars->p_full[i][hf]);
       }
       float a0, a1, b0, b1;
       tc::unpk2(sum2[0], a0, a1);
@@ -477,7 +505,28 @@ __global__ void __launch_bounds__(kQ4TcThreads, 1) q4_attend_tc_kernel(const Q4A
       const int64_t unit = ((int64_t)blockIdx.z * gridDim.y + h) * g.n_tiles + tile;
       const int64_t part = (unit * g.n_split + split) * kQ4TcRows + i * kTcRows + r;
       const float inv = l > 0.f ? 1.f / l : 0.f;
+      // 128 bytes of each of the warp's rows at a time through shared memory
+      // (this tile's Q, which no product reads any more), so that a store
+      // covers whole rows' pieces.
+      char* stage = smem + L::kQOff + i * L::kHalves * L::kHalfBytes + quarter * 4096;
+      const bool parts = g.n_split > 1;
+      auto put = [&](int chunk, uint4 v) {
+        *reinterpret_cast<uint4*>(stage + lane * 128 + ((chunk ^ (lane & 7)) * 16)) = v;
+      };
+      auto flush = [&](int piece) {
+        __syncwarp();
 #pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int rr = 4 * k + (lane >> 3), ch = lane & 7;
+          const int64_t at = __shfl_sync(0xffffffffu, orow, rr);
+          const uint4 v = *reinterpret_cast<const uint4*>(stage + rr * 128 + ((ch ^ (rr & 7)) * 16));
+          char* dst = parts ? reinterpret_cast<char*>(g.part_o + (part - lane + rr) * D)
+                            : reinterpret_cast<char*>(static_cast<__nv_bfloat16*>(g.a.o) + at * D);
+          if (unit_row - lane + rr < nrows) *reinterpret_cast<uint4*>(dst + piece * 128 + ch * 16) = v;
+        }
+        __syncwarp();
+      };
+#pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t orr[32];
         if (nt > 0) {
@@ -487,14 +536,11 @@ __global__ void __launch_bounds__(kQ4TcThreads, 1) q4_attend_tc_kernel(const Q4A
 #pragma unroll
           for (int q = 0; q < 32; ++q) orr[q] = 0;
         }
-        if (row_live && g.n_split > 1) {
-          float4* dst = reinterpret_cast<float4*>(g.part_o + part * D + c * 32);
+        if (parts) {
 #pragma unroll
-          for (int q = 0; q < 8; ++q)
-            dst[q] = make_float4(__uint_as_float(orr[4 * q]), __uint_as_float(orr[4 * q + 1]),
-                                 __uint_as_float(orr[4 * q + 2]), __uint_as_float(orr[4 * q + 3]));
-        } else if (row_live) {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(g.a.o) + orow * D + c * 32);
+          for (int q = 0; q < 8; ++q) put(q, make_uint4(orr[4 * q], orr[4 * q + 1], orr[4 * q + 2], orr[4 * q + 3]));
+          flush(c);
+        } else {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             uint32_t w[4];
@@ -502,10 +548,10 @@ __global__ void __launch_bounds__(kQ4TcThreads, 1) q4_attend_tc_kernel(const Q4A
             for (int x = 0; x < 4; ++x)
               w[x] = tc::pack_bf162(__uint_as_float(orr[8 * q + 2 * x]) * inv,
                                     __uint_as_float(orr[8 * q + 2 * x + 1]) * inv);
-            dst[q] = make_uint4(w[0], w[1], w[2], w[3]);
+            put((c & 1) * 4 + q, make_uint4(w[0], w[1], w[2], w[3]));
           }
+          if (c & 1) flush(c >> 1);
         }
-        __syncwarp();
       }
       if (row_live) {
         const float M = m * sc;
