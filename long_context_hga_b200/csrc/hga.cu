@@ -1243,13 +1243,24 @@ struct Q4Plan {
   }
 };
 
-constexpr int64_t kQ4TcMinRows = 64;
+// tcgen05 takes 256 rows at the price of one and expands K and V once for them,
+// but a CTA of it costs about 20 us to start and end.  Times in us, dense, 32
+// heads on 4, d 128, sequences x context, mma.sync / tcgen05:
+//   rows       32         64         128        256
+//   1 x 16384  20 / 51    24 / 52    34 / 53    70 / 56
+//   8 x 8192   37 / 51    84 / 52    99 / 53   182 / 61
+//   32 x 4096  59 / 75    99 / 77   178 / 78   341 / 94
+//   8 x 1024   18 / 24    25 / 24    26 / 25    35 / 28
+// so: from 64 rows on, if the 16-row tiles of mma.sync have more tokens to go
+// over than this, all together.
+constexpr int64_t kQ4TcMinRows = 64, kQ4TcMinWork = 1 << 19;
 
 // rows, max_tok: most query rows and tokens of a unit; n_seq: sequences of a
 // dense call, 0 for a routed one.
 Q4Plan q4_plan(const hga_params* p, int64_t units, int64_t rows, int64_t max_tok, int64_t n_seq) {
   Q4Plan pl;
-  pl.tc = p->dtype == HGA_BF16 && rows >= kQ4TcMinRows;
+  pl.tc = p->dtype == HGA_BF16 && rows >= kQ4TcMinRows &&
+          units * ((rows + 15) / 16) * max_tok > kQ4TcMinWork;
   pl.rows = pl.tc ? hga::kQ4TcRows : p->dtype == HGA_BF16 && rows > 8 ? 16 : 8;
   pl.n_tiles = (int)((rows + pl.rows - 1) / pl.rows);
   const int64_t ctas = std::max<int64_t>(1, units * pl.n_tiles);

@@ -215,14 +215,26 @@ def test_dense_attention(hq, hkv, d, page, dtype, seqs):
     n = int(off[-1])
     # rows behind the last sequence stay as they are
     q = torch.randn(n + 3, hq, d, generator=g, device="cuda").to(p.torch_dtype)
-    o = torch.full_like(q, 5.0)
-    lse = torch.full((n + 3, hq), 5.0, device="cuda")
     b = hga.Q4Batch(_i32(np.arange(len(seqs))), _i32(off), max(nq))
-    hga.q4_attend(p, c.pool, 0, b, q, o, lse, max_ctx=max(s[0] for s in seqs))
-    assert hga.check() == 0
-    assert torch.all(o[n:] == 5) and torch.all(lse[n:] == 5)
-    G = hq // hkv
-    q64, o64, l64 = _f64(q), _f64(o), _f64(lse)
+    q64 = _f64(q)
+    # a tight bound of the lengths and a loose one: the work is cut, and its
+    # kernel chosen, by the bound
+    for bound in (max(s[0] for s in seqs), 1 << 21):
+        o = torch.full_like(q, 5.0)
+        lse = torch.full((n + 3, hq), 5.0, device="cuda")
+        hga.q4_attend(p, c.pool, 0, b, q, o, lse, max_ctx=bound)
+        assert hga.check() == 0
+        assert torch.all(o[n:] == 5) and torch.all(lse[n:] == 5)
+        o64, l64 = _f64(o), _f64(lse)
+        _check_dense(p, c, seqs, off, q64, o64, l64, max(nq))
+        # a repeat is equal bit for bit
+        o2, lse2 = torch.full_like(o, 5.0), torch.full_like(lse, 5.0)
+        hga.q4_attend(p, c.pool, 0, b, q, o2, lse2, max_ctx=bound)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def _check_dense(p, c, seqs, off, q64, o64, l64, max_q):
+    hkv, d, G = p.n_kv_heads, p.head_dim, p.n_q_heads // p.n_kv_heads
     for i, (ctx, m) in enumerate(seqs):
         pos = ctx - m + np.arange(m)
         for h in range(hkv):
@@ -230,12 +242,7 @@ def test_dense_attention(hq, hkv, d, page, dtype, seqs):
             rows = slice(off[i], off[i + 1]), slice(h * G, (h + 1) * G)
             allowed = np.repeat(np.arange(ctx)[None] <= pos[:, None], G, 0)
             _check_row(p, o64[rows].reshape(-1, d), l64[rows].reshape(-1), q64[rows].reshape(-1, d),
-                       k, v, allowed, (i, h), max(nq))
-    # the same call once more, split otherwise and without a given workspace
-    # for the caller: equal to rounding; a repeat is equal bit for bit
-    o2, lse2 = torch.full_like(o, 5.0), torch.full_like(lse, 5.0)
-    hga.q4_attend(p, c.pool, 0, b, q, o2, lse2, max_ctx=max(s[0] for s in seqs))
-    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+                       k, v, allowed, (i, h), max_q)
 
 
 def test_inactive_rows_one_token_form_and_no_lse():
@@ -255,8 +262,8 @@ def test_inactive_rows_one_token_form_and_no_lse():
     assert torch.equal(o2, o[[0, 2]])
 
 
-@pytest.mark.parametrize("nq", [1, 40])
-def test_missing_pages_and_short_rows_are_left_out(nq):
+@pytest.mark.parametrize("nq,bound", [(1, 200), (40, 200), (40, 1 << 21)])
+def test_missing_pages_and_short_rows_are_left_out(nq, bound):
     hga = _lib()
     p = hga.Params(4, 1, 64)
     c = Cache(hga, p, [200, 50], 16)
@@ -266,7 +273,7 @@ def test_missing_pages_and_short_rows_are_left_out(nq):
     o, lse = torch.zeros_like(q), torch.zeros(2 * nq, 4, device="cuda")
     c.pool.length[1] = nq - 1                        # fewer tokens than queries
     b = hga.Q4Batch(_i32([0, 1]), _i32([0, nq, 2 * nq]), nq)
-    hga.q4_attend(p, c.pool, 0, b, q, o, lse, max_ctx=200)
+    hga.q4_attend(p, c.pool, 0, b, q, o, lse, max_ctx=bound)
     assert hga.check() == hga.HGA_ERR_DEVICE_CHECK
     k, v = c.kv(0, 0)
     pos = 200 - nq + np.arange(nq)
@@ -285,11 +292,12 @@ def test_queries_of_any_magnitude(dtype, scale):
     hga = _lib()
     p = hga.Params(8, 1, 128, dtype=dtype)
     c = Cache(hga, p, [150], 64)
-    for nq in (1, 100):
+    for nq, bound in ((1, 150), (100, 150), (100, 1 << 21)):
         q = (torch.randn(nq, 8, 128, device="cuda") * scale).to(p.torch_dtype)
         q[:, 3] = 0                                  # a zero row
         o, lse = torch.zeros_like(q), torch.zeros(nq, 8, device="cuda")
-        hga.q4_attend(p, c.pool, 0, hga.Q4Batch(_i32([0]), _i32([0, nq]), nq), q, o, lse, max_ctx=150)
+        hga.q4_attend(p, c.pool, 0, hga.Q4Batch(_i32([0]), _i32([0, nq]), nq), q, o, lse,
+                      max_ctx=bound)
         assert hga.check() == 0
         k, v = c.kv(0, 0)
         allowed = np.repeat(np.arange(150)[None] <= (150 - nq + np.arange(nq))[:, None], 8, 0)
@@ -328,6 +336,9 @@ def _lists(hga, p, q0, n, t_cap, rng, fill):
     (4, 2, 64, 32, "fp32", 320, 100, 64, 64, 8, None),
     (4, 4, 128, 64, "fp32", 320, 3, 64, 64, 8, 322),
     (2, 1, 128, 128, "bf16", 1024, 64, 64, 0, 0, None),         # every group
+    (32, 4, 128, 64, "bf16", 4096, 500, 64, 512, 64, None),
+    (32, 4, 64, 8, "bf16", 4096, 450, 64, 512, 64, 4170),
+    (40, 4, 128, 16, "bf16", 2048, 390, 0, 512, 64, None),      # 10 heads a KV head
 ])
 def test_routed_attention(hq, hkv, d, page, dtype, q0, n, sink, local, top, pos_lo):
     hga = _lib()
@@ -470,7 +481,7 @@ def test_pages_far_into_a_large_pool():
     ko, vo = torch.zeros_like(k), torch.zeros_like(v)
     hga.q4_read(p, pool, 0, b, ko, vo)
     o, lse = torch.zeros_like(q), torch.zeros(150, 8, device="cuda")
-    hga.q4_attend(p, pool, 0, b, q, o, lse)
+    hga.q4_attend(p, pool, 0, b, q, o, lse, max_ctx=1 << 21)
     assert hga.check() == 0
     k64, v64 = q4_ref.stored(_f64(k)), q4_ref.stored(_f64(v))
     assert np.array_equal(_f64(ko), k64) and np.array_equal(_f64(vo), v64)
