@@ -644,8 +644,8 @@ hga_status hga_q4_read(const hga_params* p, const hga_page_pool* pool, int32_t p
 /* Dense causal attention of the batch's tokens: the query at position pos of a
  * sequence attends its tokens [0, pos].  q, o: [n_tok][n_q_heads][head_dim] in
  * dtype, lse [n_tok][n_q_heads] float32 or NULL.  max_ctx: an upper bound of
- * the sequences' lengths (sizes the split of long contexts; results stay right
- * beyond it).  work: device, 16-byte aligned, hga_q4_attend_work(...) bytes,
+ * the sequences' lengths (how the work is cut follows from it, max_q and n_seq;
+ * results stay right beyond it).  work: device, 16-byte aligned, hga_q4_attend_work(...) bytes,
  * not shared by calls that may overlap.  A sequence with fewer tokens than
  * queries sets HGA_ERR_DEVICE_CHECK and gives 0 and -inf; so do missing pages,
  * whose tokens are left out, and a sequence of more than max_q tokens or with

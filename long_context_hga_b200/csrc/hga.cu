@@ -1142,8 +1142,9 @@ hga_status check_pool(const hga_page_pool* p, bool data) {
       p->plane_stride / p->page_bytes < p->n_pages)
     return HGA_ERR_INVALID_ARG;
   if ((data && !p->data) || !aligned16(p->data)) return HGA_ERR_INVALID_ARG;
-  // positions, page ranks and table entries are counted in 32 bits
-  if ((int64_t)p->row_pages * p->page_tokens > 0x7fffffff || p->n_pages > 1 << 30 ||
+  // positions, page ranks and table entries are counted in 32 bits (positions
+  // with room for a rounding up to whole steps)
+  if ((int64_t)p->row_pages * p->page_tokens > 0x7ffff000 || p->n_pages > 1 << 30 ||
       (int64_t)p->n_rows * p->row_pages > 0x7fffffff)
     return HGA_ERR_UNSUPPORTED;
   return HGA_OK;

@@ -21,7 +21,10 @@
 //
 // A tile's chain is softmax, P V, next S; while one tile is in softmax the
 // other's products run.  P V starts on the first 64 tokens while the others'
-// weights are computed.
+// weights are computed.  Bound: that chain (a step takes 4200 cycles, its
+// products 2048).  3 sequences of up to 1K tokens on up to 8K, 32 heads on 8, d
+// 128, with the append: 380 us, 0.48 of the bf16 rate; routed, 2K queries of a
+// 64K context, 32 heads on 4: 64 us.
 //
 // Weights are held as 2^7 exp(score - m), m the running maximum, which is only
 // moved when it grows by more than 2^8 (so that O is rarely rescaled): at most
@@ -262,12 +265,15 @@ __global__ void __launch_bounds__(kQ4TcThreads, 1) q4_attend_tc_kernel(const Q4A
           if (x == s) last_use[x] = u_s;
         look(n + 2);
       }
-      // no copy may still be landing when the block's memory goes: the expanding
-      // warps have waited for every one, unless the block gives up
-      if ((gave_up || *abort_flag) && lane == 0) {
+      // no copy may still be landing when the block's memory goes: a stage's
+      // last load is waited for (a stage that the other warp filled again was
+      // waited for by the expanding warps; a block that gives up waits for what
+      // this warp issued, or for the limit)
+      if (lane == 0) {
 #pragma unroll
         for (int x = 0; x < L::kStages; ++x) {
           if (last_use[x] < 0) continue;
+          if (!gave_up && last_use[x] * L::kStages + x < 2 * nt - L::kStages) continue;
           const uint64_t t0 = tc::globaltimer_ns();
           while (!tc::mbar_try_wait(&bars->raw_full[x], last_use[x] & 1) &&
                  tc::globaltimer_ns() - t0 < tc::kWaitLimitNs) {

@@ -1030,10 +1030,12 @@ def q4_read(p: Params, pool: PagePool, plane: int, batch: Q4Batch, k, v, stream=
 
 
 def _work(n_bytes: int, device, stream):
-    w = torch.empty(n_bytes, dtype=torch.uint8, device=device)
-    if stream is not None:
-        w.record_stream(stream)
-    return w
+    """Workspace of one call, in the memory pool of the call's stream: neither an
+    earlier user of the memory on another stream nor the next one can overlap it."""
+    if stream is None:
+        return torch.empty(n_bytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(n_bytes, dtype=torch.uint8, device=device)
 
 
 def q4_workspace(p: Params, batch: Q4Batch, n_tok: int, max_ctx: int) -> Optional[torch.Tensor]:
