@@ -202,20 +202,25 @@ __device__ __forceinline__ int q4_entry(const Q4List& x, int i) {
   return r < x.n_l ? x.loc0 + r : x.d0 + r - x.n_l;
 }
 
-// Byte offset of a record from the plane's first page, -1 (reported) where the
-// page table names none.
-__device__ __forceinline__ int64_t q4_where(const Q4Cache& c, const int32_t* pages, int h, int ent,
-                                            int rec_bytes) {
+// Where a record lies, in two halves so that nothing waits for the page table
+// until a step later: its page (as the table says, -1 past the row) and its index
+// in the page; then the byte offset from the plane's first page, -1 (reported)
+// where the table names none.
+__device__ __forceinline__ int q4_page_of(const Q4Cache& c, const int32_t* pages, int ent, int* in) {
   // ent / page_recs by the reciprocal, off by at most one
-  int col = (int)__umulhi((uint32_t)ent, c.page_recs_inv), in = ent - col * c.page_recs;
-  if (in < 0) --col, in += c.page_recs;
-  else if (in >= c.page_recs) ++col, in -= c.page_recs;
-  const int pg = col < c.row_pages ? pages[col] : -1;
-  if (pg < 0 || pg >= c.n_pages) {
+  int col = (int)__umulhi((uint32_t)ent, c.page_recs_inv);
+  *in = ent - col * c.page_recs;
+  if (*in < 0) --col, *in += c.page_recs;
+  else if (*in >= c.page_recs) ++col, *in -= c.page_recs;
+  return col < c.row_pages ? pages[col] : -1;
+}
+__device__ __forceinline__ int64_t q4_offset(const Q4Cache& c, int h, int page, int in,
+                                             int rec_bytes) {
+  if (page < 0 || page >= c.n_pages) {
     report(HGA_ERR_DEVICE_CHECK);
     return -1;
   }
-  return pg * c.page_bytes + ((int64_t)h * c.page_recs + in) * rec_bytes;
+  return page * c.page_bytes + ((int64_t)h * c.page_recs + in) * rec_bytes;
 }
 
 // Fetches up to 8 records (lane e < 8 holds record e's offset, -1 for none) to
@@ -354,16 +359,16 @@ __global__ void __launch_bounds__(32 * kQ4Warps, (q4_ctas<NT, T>())) q4_attend_k
   const int n_mine = hi > lo + warp ? (hi - lo - warp + kQ4Warps - 1) / kQ4Warps : 0;
   unsigned got[kQ4Stages];                      // records that were fetched, per stage
   int issued = 0;
-  int ent = -1;                                 // this lane's record of the next fetch
-  int64_t at = -1;
+  int ent = -1, page = -1, in = 0;              // this lane's record of the next fetch
   auto look = [&](int i) {
     ent = i < n_mine && lane < kQ4StepRecs
               ? q4_entry<ROUTED>(list, (lo + warp + i * kQ4Warps) * kQ4StepRecs + lane)
               : -1;
-    at = ent >= 0 ? q4_where(g.c, pages, h, ent, L::kRec) : -1;
+    if (ent >= 0) page = q4_page_of(g.c, pages, ent, &in);
   };
   // Fetches step i; its places were looked up during the step before.
   auto fetch = [&](int i, int s) -> unsigned {
+    const int64_t at = ent >= 0 ? q4_offset(g.c, h, page, in, L::kRec) : -1;
     if (lane < kQ4StepRecs) ents[s * 8 + lane] = at >= 0 ? ent : -1;
     const unsigned m = __ballot_sync(0xffffffffu, at >= 0);
     ++issued;

@@ -191,6 +191,17 @@ __global__ void __launch_bounds__(kQ4TcThreads, 1) q4_attend_tc_kernel(const Q4A
   const int first_pos = u.pos0 + row0 / G;
   const int last_pos = u.pos0 + min(nrows - 1, row0 + kQ4TcRows - 1) / G;
 
+  if (warp >= 8) {
+    // q's row on its way into L2 while the block sets up
+    const int ur = row0 + tid - 256;
+    if (ur < nrows) {
+      const char* src = reinterpret_cast<const char*>(
+          static_cast<const __nv_bfloat16*>(g.a.q) +
+          ((u.tok0 + ur / G) * g.a.Hq + (int64_t)h * G + ur % G) * D);
+#pragma unroll
+      for (int x = 0; x < D * 2; x += 128) asm volatile("prefetch.global.L2 [%0];\n" ::"l"(src + x));
+    }
+  }
   if (tid == 0) {
     bars->abort = 0;
     tc::mbar_init(&bars->q_full, nq * 4);
@@ -238,11 +249,10 @@ __global__ void __launch_bounds__(kQ4TcThreads, 1) q4_attend_tc_kernel(const Q4A
       int last_use[L::kStages];
 #pragma unroll
       for (int s = 0; s < L::kStages; ++s) last_use[s] = -1;
-      int ent = -1;
-      int64_t at = -1;
+      int ent = -1, page = -1, in = 0;
       auto look = [&](int n) {
         ent = lane < 8 && n < 2 * nt ? q4_entry<ROUTED>(list, t_lo * 16 + n * 8 + lane) : -1;
-        at = ent >= 0 ? q4_where(g.c, pages, h, ent, q4_record_bytes(D)) : -1;
+        if (ent >= 0) page = q4_page_of(g.c, pages, ent, &in);
       };
       bool gave_up = false;
       look(warp - 1);
@@ -255,6 +265,7 @@ __global__ void __launch_bounds__(kQ4TcThreads, 1) q4_attend_tc_kernel(const Q4A
         // slot was read by the softmax of step j - 4, which is done once the
         // first half of step j - 2 is expanded (that waits for the slots of
         // step j - 4)
+        const int64_t at = ent >= 0 ? q4_offset(g.c, h, page, in, q4_record_bytes(D)) : -1;
         const unsigned live = __ballot_sync(0xffffffffu, at >= 0);
         if (lane < 8) ents[(n & 7) * 8 + lane] = at >= 0 ? ent : -1;
         if (lane == 0) flags[n & 7] = live != 0xffu;
@@ -363,22 +374,19 @@ __global__ void __launch_bounds__(kQ4TcThreads, 1) q4_attend_tc_kernel(const Q4A
                                         (((x & 7) ^ (rr & 7)) * 16));
       };
       const int x = lane % kLanes;
+      uint4 raw[kLanes];
 #pragma unroll
-      for (int it0 = 0; it0 < kLanes; it0 += 8) {
-        uint4 raw[8];
-#pragma unroll
-        for (int it = 0; it < 8; ++it) {
-          const int rr = (it0 + it) * kAt + lane / kLanes;
-          const int64_t at = __shfl_sync(0xffffffffu, orow, rr);
-          raw[it] = make_uint4(0, 0, 0, 0);
-          if (unit_row - lane + rr < nrows)
-            raw[it] = *reinterpret_cast<const uint4*>(
-                static_cast<const __nv_bfloat16*>(g.a.q) + at * D + x * 8);
-        }
-#pragma unroll
-        for (int it = 0; it < 8; ++it)
-          *chunk(quarter * 32 + (it0 + it) * kAt + lane / kLanes, x) = raw[it];
+      for (int it = 0; it < kLanes; ++it) {
+        const int rr = it * kAt + lane / kLanes;
+        const int64_t at = __shfl_sync(0xffffffffu, orow, rr);
+        raw[it] = make_uint4(0, 0, 0, 0);
+        if (unit_row - lane + rr < nrows)
+          raw[it] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(g.a.q) + at * D +
+                                                    x * 8);
       }
+#pragma unroll
+      for (int it = 0; it < kLanes; ++it)
+        *chunk(quarter * 32 + it * kAt + lane / kLanes, x) = raw[it];
       __syncwarp();
       uint32_t top = 0;
 #pragma unroll 4
@@ -394,8 +402,8 @@ __global__ void __launch_bounds__(kQ4TcThreads, 1) q4_attend_tc_kernel(const Q4A
       sc = __uint_as_float((uint32_t)ex << 23) * g.a.scale_log2;
 #pragma unroll 4
       for (int y = 0; y < kLanes; ++y) {
-        const uint4 raw = *chunk(r, y);
-        const uint32_t v[4] = {raw.x, raw.y, raw.z, raw.w};
+        const uint4 in = *chunk(r, y);
+        const uint32_t v[4] = {in.x, in.y, in.z, in.w};
         uint32_t o[4];
 #pragma unroll
         for (int w = 0; w < 4; ++w)
