@@ -546,7 +546,9 @@ typedef struct hga_page_pool {
   int32_t n_planes;
   int32_t page_tokens;   /* a multiple of 8                                     */
   int32_t n_rows;
-  int32_t row_pages;     /* entries of a table row                              */
+  int32_t row_pages;     /* entries of a table row; row_pages * page_tokens is  */
+                         /* below 2^31 - 4096, n_rows * row_pages below 2^31,   */
+                         /* n_pages at most 2^30 (HGA_ERR_UNSUPPORTED)          */
   int32_t* table;        /* [n_rows][row_pages]                                 */
   int32_t* len;          /* [n_rows]                                            */
   int32_t* ref;          /* [n_pages]                                           */

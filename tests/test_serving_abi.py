@@ -113,7 +113,10 @@ def test_pages_refuse(hga):
         assert call(ok, -1) == 1
         assert call(ok, 1, None) == 1
         assert call(ok, 17 if name == "copy" else 5) == 1   # longer than the pool allows
-        assert call(B(_pool(hga, row_pages=1 << 30, page_tokens=64)), 1) == 2
+        for big in (dict(row_pages=1 << 30, page_tokens=64), dict(row_pages=1, page_tokens=(1 << 31) - 4088),
+                    dict(n_rows=1 << 20, row_pages=1 << 11, page_tokens=8),
+                    dict(n_pages=(1 << 30) + 1, plane_stride=1 << 62)):
+            assert call(B(_pool(hga, **big)), 1) == 2, (name, big)
     assert L.hga_pages_copy(B(_pool(hga, data=None)), FAKE, FAKE, 1, None) == 1
     assert L.hga_pages_compact(None, None) == 1
     for bad in BAD_POOLS + (dict(work=None),):
