@@ -1169,13 +1169,15 @@ hga_status pool_args(const hga_page_pool* p, hga::PoolArgs* a) {
   return HGA_OK;
 }
 
-// Blocks of a page copy whose size only the device may know.
+// 16 KB turns of n page copies.
 int64_t copy_turns(const hga::PoolArgs& a, int64_t n) {
   return (a.page_bytes / 16 + 4 * hga::kCopyThreads - 1) / (4 * hga::kCopyThreads) * a.n_planes * n;
 }
+// Blocks of a page copy whose size only the device may know (four times what an
+// SM holds: 128 copies in 36 planes 77 us against 81 with one wave).
 unsigned copy_grid(const hga::PoolArgs& a, int64_t n) {
   const int64_t total = std::max<int64_t>(1, copy_turns(a, n));
-  return (unsigned)std::min<int64_t>(std::max<int64_t>(total, n), 148 * 8);
+  return (unsigned)std::min<int64_t>(std::max<int64_t>(total, n), 148 * 32);
 }
 
 hga_status q4_cache(const hga_params* p, const hga_page_pool* pool, int32_t plane,
