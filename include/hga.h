@@ -106,7 +106,8 @@ typedef struct hga_params {
                         /* its inputs.  1 promises that q is complete before */
                         /* that kernel can let its dependents start (kernels */
                         /* that never do so early, such as PyTorch's, and    */
-                        /* this library's own kernels qualify); the          */
+                        /* this library's own kernels qualify: those that    */
+                        /* write q, hga_rope's, end first); the              */
                         /* tensor-core routing and attention kernels then    */
                         /* request q before the wait, overlapping its load   */
                         /* with the previous kernel's tail.  0: q is read    */

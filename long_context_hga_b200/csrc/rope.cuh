@@ -153,7 +153,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
     RopeVec<TO, VEC>::store(dst + ax, x);
     RopeVec<TO, VEC>::store(dst + ay, y);
   }
-  griddep_launch();
+  // No griddep_launch: this kernel writes q, which a call with q_ready reads
+  // without waiting, so its dependents start once all its blocks have ended.
 }
 
 }  // namespace hga
