@@ -322,6 +322,7 @@ __global__ void __launch_bounds__(32 * kQ4Warps, (q4_ctas<NT, T>())) q4_attend_k
     for (int s = 0; s < kQ4Stages; ++s) tc::mbar_init(&bars[s], 1);
     tc::fence_mbar_init();
   }
+  __syncthreads();                              // every warp's waits read s_abort
   griddep_wait();
   const int h = blockIdx.y;
   const int n_x = !ROUTED && g.slots ? g.slots : g.n_split;

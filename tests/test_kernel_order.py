@@ -25,3 +25,14 @@ def test_a_kernel_that_writes_q_lets_no_dependent_start():
     """params.q_ready lets a kernel read q before it waits for the kernel ahead
     of it, so one that writes q must not let its dependents start early."""
     assert "griddep_launch" not in _function("rope.cuh", "rope_kernel")
+
+
+def test_the_abort_flag_is_cleared_before_any_warp_reads_it():
+    """Thread 0 clears the block's abort flag; a warp that polled it before the
+    store is ordered would take what an earlier block left for an abort and
+    drop its tokens."""
+    body = _function("q4_attend.cuh", "q4_attend_kernel")
+    cleared = body.index("s_abort = 0")
+    barrier = body.index("__syncthreads()", cleared)
+    assert barrier < body.index("return", cleared)
+    assert barrier < body.index("&s_abort", cleared)
