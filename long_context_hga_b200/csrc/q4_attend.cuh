@@ -226,13 +226,16 @@ __device__ __forceinline__ int64_t q4_offset(const Q4Cache& c, int h, int page, 
 // Fetches up to 8 records (lane e < 8 holds record e's offset, -1 for none) to
 // dst + e * rec.  Records that follow one another in memory come in one copy:
 // a copy's cost is in its issue (one of 576 or 1152 bytes per record kept the
-// expanding warps of q4_attend_tc.cuh waiting for 60% of the time).  Arms bar.
+// expanding warps of q4_attend_tc.cuh waiting for 60% of the time).  Arms bar:
+// lane 0's arrive comes after every lane's stores so far (other warps read the
+// load's entries once bar completes, which is at once where no record is there).
 __device__ __forceinline__ void q4_fetch8(char* dst, const char* base, int64_t at, int rec,
                                           uint64_t* bar, int lane) {
   const int64_t before = __shfl_up_sync(0xffffffffu, at, 1);
   const unsigned live = __ballot_sync(0xffffffffu, at >= 0);
   const bool first = at >= 0 && (lane == 0 || before < 0 || at != before + rec);
   const unsigned stops = __ballot_sync(0xffffffffu, first) | ~live;
+  __syncwarp();
   if (lane == 0) tc::mbar_arrive_expect_tx(bar, __popc(live) * rec);
   __syncwarp();
   if (first) {

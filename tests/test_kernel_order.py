@@ -36,3 +36,16 @@ def test_the_abort_flag_is_cleared_before_any_warp_reads_it():
     barrier = body.index("__syncthreads()", cleared)
     assert barrier < body.index("return", cleared)
     assert barrier < body.index("&s_abort", cleared)
+
+
+def test_a_load_is_announced_after_every_lanes_entries():
+    """The lanes of a fetching warp write the load's entries, lane 0 arrives for
+    all of them: shuffles and ballots between do not order memory, so a
+    __syncwarp has to stand before the arrive."""
+    fetch = _function("q4_attend.cuh", "q4_fetch8")
+    assert "__syncwarp()" in fetch[:fetch.index("mbar_arrive_expect_tx")]
+    # and the entries are written before that call
+    for file, kernel in (("q4_attend_tc.cuh", "q4_attend_tc_kernel"),
+                         ("q4_attend.cuh", "q4_attend_kernel")):
+        body = _function(file, kernel)
+        assert 0 <= re.search(r"ents\[[^;]*\] = at", body).start() < body.index("q4_fetch8(")
