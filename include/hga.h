@@ -652,7 +652,10 @@ hga_status hga_q4_read(const hga_params* p, const hga_page_pool* pool, int32_t p
  * not shared by calls that may overlap.  A sequence with fewer tokens than
  * queries sets HGA_ERR_DEVICE_CHECK and gives 0 and -inf; so do missing pages,
  * whose tokens are left out, and a sequence of more than max_q tokens or with
- * rows past n_tok, whose outputs stay as they are.  Results do not depend on timing. */
+ * rows past n_tok, whose outputs stay as they are.  A query that is not finite
+ * gives NaN in its row of o and lse and sets HGA_ERR_DEVICE_CHECK (one that
+ * attends nothing gives 0 and -inf all the same); a score beyond +-2.3e38, whose
+ * row is then not defined, sets it too.  Results do not depend on timing. */
 hga_status hga_q4_attend(const hga_params* p, const hga_page_pool* pool, int32_t plane,
                          const hga_q4_batch* b, int64_t n_tok, const void* q, int64_t max_ctx,
                          void* o, float* lse, void* work, int64_t work_bytes,
@@ -665,8 +668,8 @@ int64_t hga_q4_attend_work(const hga_params* p, int32_t n_seq, int32_t max_q, in
  * n_q, group_idx, group_cnt, o and lse as in hga_attend, with t_cap the capacity
  * that the index arrays were made for.  Rows of positions before pos_lo are left
  * as they are (a decode step attends its last row only: pos_lo = q_start + n_q
- * - 1; q_start computes every row).  work as above,
- * hga_q4_attend_routed_work(...) bytes. */
+ * - 1; q_start computes every row).  Queries that are not finite: as in
+ * hga_q4_attend.  work as above, hga_q4_attend_routed_work(...) bytes. */
 hga_status hga_q4_attend_routed(const hga_params* p, const hga_page_pool* pool, int32_t plane,
                                 int32_t row, const void* q, int64_t q_start, int64_t n_q,
                                 int64_t pos_lo, int64_t t_cap, const int32_t* group_idx,

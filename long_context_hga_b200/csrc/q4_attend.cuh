@@ -98,6 +98,18 @@ __device__ __forceinline__ uint32_t split_half2(float x, float y, uint32_t* lo) 
   return hi;
 }
 
+// A row's maximum M (log2 units) and sum of weights S.  A row that attends
+// nothing has S = 0; a query that is not finite makes S NaN, and with it the
+// output and lse; a score that fp32 does not hold makes M infinite.
+__device__ __forceinline__ bool q4_nonfinite(float M, float S) {
+  return S != 0.f && !(fabsf(M) + S <= 3.0e38f);
+}
+__device__ __forceinline__ float q4_inverse(float S) { return S == 0.f ? 0.f : 1.f / S; }
+// shift: log2 of the factor that weights and their sums carry.
+__device__ __forceinline__ float q4_lse(float M, float S, float shift) {
+  return S == 0.f ? -INFINITY : (M + (log2f(S) - shift)) * 0.6931471805599453f;
+}
+
 // A unit's position in the batch, from the block index.
 struct Q4Unit {
   int row;                 // table row, < 0: nothing to attend (outputs 0 and -inf)
@@ -407,10 +419,12 @@ __global__ void __launch_bounds__(32 * kQ4Warps, (q4_ctas<NT, T>())) q4_attend_k
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
     // 2^-e and 2^e with the row's maximum in [1, 2) after scaling (e in
-    // [-126, 126]; a zero row takes 1)
+    // [-126, 126]; a zero row takes 1; a row with an infinity becomes NaN, as
+    // its softmax is)
     int ex = (int)((__float_as_uint(mx) >> 23) & 0xff);
+    const bool inf = ex == 255;
     ex = mx == 0.f ? 127 : min(max(ex, 1), 253);
-    const float down = __uint_as_float((uint32_t)(254 - ex) << 23);
+    const float down = __uint_as_float(inf ? 0x7fffffffu : (uint32_t)(254 - ex) << 23);
     const float up = __uint_as_float((uint32_t)ex << 23);
 #pragma unroll
     for (int j = 0; j < KS; ++j)
@@ -671,7 +685,11 @@ __global__ void __launch_bounds__(32 * kQ4Warps, (q4_ctas<NT, T>())) q4_attend_k
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const int r = nt * 8 + 2 * t + x;
-        if (gr == 0) jm[warp * R + r] = make_float2(m[nt][x] * sc[nt][x], l[nt][x]);
+        if (gr == 0) {
+          const float M = m[nt][x] * sc[nt][x];
+          if (q4_nonfinite(M, l[nt][x])) report(HGA_ERR_DEVICE_CHECK);
+          jm[warp * R + r] = make_float2(M, l[nt][x]);
+        }
         float* dst = jo + (warp * R + r) * D + gr * (D / 8);
 #pragma unroll
         for (int j = 0; j < KS; ++j)
@@ -701,14 +719,14 @@ __global__ void __launch_bounds__(32 * kQ4Warps, (q4_ctas<NT, T>())) q4_attend_k
       if (c == 0) g.part_ml[at] = make_float2(M, S);
       continue;
     }
-    const float inv = S > 0.f ? 1.f / S : 0.f;
+    const float inv = q4_inverse(S);
     const int64_t orow = (u.tok0 + pr / g.a.G) * g.a.Hq + (int64_t)h * g.a.G + pr % g.a.G;
     T* dst = static_cast<T*>(g.a.o) + orow * D + c;
     dst[0] = Elt<T>::from_f32(acc.x * inv);
     dst[1] = Elt<T>::from_f32(acc.y * inv);
     dst[2] = Elt<T>::from_f32(acc.z * inv);
     dst[3] = Elt<T>::from_f32(acc.w * inv);
-    if (c == 0 && g.a.lse) g.a.lse[orow] = S > 0.f ? (M + (log2f(S) - kQ4PShift)) * 0.6931471805599453f : -INFINITY;
+    if (c == 0 && g.a.lse) g.a.lse[orow] = q4_lse(M, S, kQ4PShift);
   }
   griddep_launch();
 }
@@ -785,14 +803,13 @@ __global__ void __launch_bounds__(128) q4_join_kernel(const Q4AttendArgs g) {
         acc[i] = (s_acc[0][lane * V + i] + s_acc[1][lane * V + i]) +
                  (s_acc[2][lane * V + i] + s_acc[3][lane * V + i]);
     }
-    const float inv = S > 0.f ? 1.f / S : 0.f;
+    const float inv = q4_inverse(S);
     const int pr = row0 + r;
     const int64_t orow = (u.tok0 + pr / g.a.G) * g.a.Hq + (int64_t)h * g.a.G + pr % g.a.G;
     T* dst = static_cast<T*>(g.a.o) + orow * D + lane * V;
 #pragma unroll
     for (int i = 0; i < V; ++i) dst[i] = Elt<T>::from_f32(acc[i] * inv);
-    if (lane == 0 && g.a.lse)
-      g.a.lse[orow] = S > 0.f ? (M + (log2f(S) - g.shift)) * 0.6931471805599453f : -INFINITY;
+    if (lane == 0 && g.a.lse) g.a.lse[orow] = q4_lse(M, S, g.shift);
   }
   griddep_launch();
 }

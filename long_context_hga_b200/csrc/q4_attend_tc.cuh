@@ -398,7 +398,8 @@ __global__ void __launch_bounds__(kQ4TcThreads, 1) q4_attend_tc_kernel(const Q4A
       top = max(top & 0xffffu, top >> 16);
       int ex = (int)(top >> 7);
       ex = top == 0 ? 127 : min(max(ex, 1), 253);
-      const float down = __uint_as_float((uint32_t)(254 - ex) << 23);
+      // a row with an infinity or NaN becomes NaN, as its softmax is
+      const float down = __uint_as_float(top >= 0x7f80u ? 0x7fffffffu : (uint32_t)(254 - ex) << 23);
       sc = __uint_as_float((uint32_t)ex << 23) * g.a.scale_log2;
 #pragma unroll 4
       for (int y = 0; y < kLanes; ++y) {
@@ -513,12 +514,14 @@ __global__ void __launch_bounds__(kQ4TcThreads, 1) q4_attend_tc_kernel(const Q4A
     if (ok && nt > 0) {
       ok = tc::mbar_wait_warp(&bars->o_full[i], (nt - 1) & 1, abort_flag);
       tc::fence_after_sync();
-      if (m == -INFINITY) l = 0.f;              // no token: the polynomial's 2^-125 are not weights
+      // no token: the polynomial's 2^-125 are not weights (NaN scores leave m too,
+      // but l is NaN then: no record's first token is a polynomial's column)
+      if (m == -INFINITY && l == l) l = 0.f;
     }
     if (ok && (g.n_split == 1 || nt > 0 || split == 0)) {
       const int64_t unit = ((int64_t)blockIdx.z * gridDim.y + h) * g.n_tiles + tile;
       const int64_t part = (unit * g.n_split + split) * kQ4TcRows + i * kTcRows + r;
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float inv = q4_inverse(l);
       // 128 bytes of each of the warp's rows at a time through shared memory
       // (this tile's Q, which no product reads any more), so that a store
       // covers whole rows' pieces.
@@ -569,9 +572,9 @@ __global__ void __launch_bounds__(kQ4TcThreads, 1) q4_attend_tc_kernel(const Q4A
       }
       if (row_live) {
         const float M = m * sc;
+        if (q4_nonfinite(M, l)) report(HGA_ERR_DEVICE_CHECK);
         if (g.n_split > 1) g.part_ml[part] = make_float2(M, l);
-        else if (g.a.lse)
-          g.a.lse[orow] = l > 0.f ? (M + (log2f(l) - kQ4TcShift)) * 0.6931471805599453f : -INFINITY;
+        else if (g.a.lse) g.a.lse[orow] = q4_lse(M, l, kQ4TcShift);
       }
     }
   }
