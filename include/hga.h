@@ -626,8 +626,9 @@ int64_t hga_q4_page_bytes(const hga_params* p, int32_t page_tokens);
 
 /* Stores the K and V of the batch's tokens.  k, v: dtype, value d of head h of
  * packed token t at k[t * k_token_stride + h * k_head_stride + d]; 16-byte
- * aligned, strides multiples of 16 bytes.  n_tok: packed rows.  A position the
- * row has no page for, or a row named by two sequences, sets
+ * aligned, strides multiples of 16 bytes.  n_tok: packed rows.  At most 65535
+ * sequences (HGA_ERR_UNSUPPORTED; also in hga_q4_attend).  A position the row has
+ * no page for, or a row named by two sequences that have tokens, sets
  * HGA_ERR_DEVICE_CHECK.  The pages written must not be shared (hga_pages_fork
  * leaves the page being filled to one row). */
 hga_status hga_q4_append(const hga_params* p, const hga_page_pool* pool, int32_t plane,

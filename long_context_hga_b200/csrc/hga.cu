@@ -1467,6 +1467,7 @@ hga_status hga_q4_append(const hga_params* p, const hga_page_pool* pool, int32_t
   hga_status s = q4_io_args(p, pool, plane, b, n_tok, k, k_token_stride, k_head_stride, v,
                             v_token_stride, v_head_stride, e, e, &a);
   if (s != HGA_OK || n_tok == 0 || b->n_seq == 0) return s;
+  if (b->n_seq > 65535) return HGA_ERR_UNSUPPORTED;   // as hga_q4_attend
   const dim3 grid(q4_io_grid(&a));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return p->dtype == HGA_BF16
