@@ -515,8 +515,9 @@ typedef struct hga_rope_io {
 
 /* Rotates q and (when k is not NULL) k of n tokens in one launch.  pos: device
  * int32, the position of token t on axis a at pos[a * pos_stride + t],
- * pos_stride >= n.  k's output strides may be those of a [n_kv_heads][t_cap]
- * [head_dim] cache.  An axis[i] >= n_axes sets HGA_ERR_DEVICE_CHECK. */
+ * pos_stride >= n, or 0: one position for all axes.  k's output strides may be
+ * those of a [n_kv_heads][t_cap][head_dim] cache.  An axis[i] >= n_axes sets
+ * HGA_ERR_DEVICE_CHECK. */
 hga_status hga_rope(const hga_rope_plan* r, const int32_t* pos, int64_t pos_stride, int64_t n,
                     const hga_rope_io* q, const hga_rope_io* k, hga_stream_t stream);
 

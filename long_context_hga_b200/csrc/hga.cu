@@ -1083,7 +1083,7 @@ hga_status rope_common(const hga_rope_plan* r, const int32_t* pos, int64_t pos_s
   if (r->n_axes < 1 || r->head_dim < 1 || r->rot_dim < 0 || r->rot_dim % 2 ||
       r->rot_dim > r->head_dim || (r->adjacent != 0 && r->adjacent != 1))
     return HGA_ERR_INVALID_ARG;
-  if (n < 0 || pos_stride < n) return HGA_ERR_INVALID_ARG;
+  if (n < 0 || (pos_stride < n && pos_stride != 0)) return HGA_ERR_INVALID_ARG;
   const hga_rope_io* ios[2] = {q, k};
   hga::RopeArgs a{};
   const int half = r->rot_dim / 2;

@@ -30,7 +30,7 @@ struct RopeIo {
 struct RopeArgs {
   const double* freq;       // [half]
   const uint8_t* axis;      // [half]
-  const int32_t* pos;       // [n_axes][pos_stride]
+  const int32_t* pos;       // [n_axes][pos_stride] (stride 0: the same for all axes)
   int64_t pos_stride, n;
   int n_axes, half, d, adjacent;
   int heads0, heads;        // heads of io[0], heads of both

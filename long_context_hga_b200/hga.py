@@ -863,10 +863,10 @@ def _rope(what: str, fn, plan: Rope, pos, q, q_out, k, k_out, stream):
 
 def rope(plan: Rope, pos, q, q_out, k=None, k_out=None, stream=None):
     """Rotates q [n, Hq, d] into q_out and k [n, Hkv, d] into k_out at the
-    positions pos (int32 [n_axes, n]; [n] for one axis).  Any token and head
-    strides: q and k may be views of a fused projection, k_out the view
-    cache[:, t0:t0 + n].transpose(0, 1) of a [Hkv, t_cap, d] cache; out may be
-    the input itself."""
+    positions pos (int32 [n_axes, n]; [n] for one axis, [n] expanded for the
+    same on all).  Any token and head strides: q and k may be views of a fused
+    projection, k_out the view cache[:, t0:t0 + n].transpose(0, 1) of a [Hkv,
+    t_cap, d] cache; out may be the input itself."""
     _rope("hga_rope", LIB.hga_rope, plan, pos, q, q_out, k, k_out, stream)
 
 
