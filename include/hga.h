@@ -572,8 +572,10 @@ hga_status hga_pages_reserve(const hga_page_pool* pool, const int32_t* rows,
  * lowest free one, so that both can grow.  Refused: rows outside the table, a
  * child that is not empty (length 0) or listed before, a parent that is also a
  * child of the call; when the pages run out, that entry and every later one
- * that needs a page.  n <= n_rows.  A row's whole pages are never written
- * again; a row must not shrink while it shares pages. */
+ * that needs a page.  A whole page that the parent's table lacks (set from
+ * outside) is reported and lacking in the child too.  n <= n_rows.  A row's
+ * whole pages are never written again; a row must not shrink while it shares
+ * pages. */
 hga_status hga_pages_fork(const hga_page_pool* pool, const int32_t* parents,
                           const int32_t* children, int32_t n, hga_stream_t stream);
 

@@ -1118,9 +1118,9 @@ hga_status rope_common(const hga_rope_plan* r, const int32_t* pos, int64_t pos_s
   a.adjacent = r->adjacent;
   a.heads0 = q->heads;
   a.heads = q->heads + (k ? k->heads : 0);
-  // about 2048 blocks, fewer tokens in each of a shorter call (4096 tokens, 40
-  // heads of 128: 2 tokens a block 35 us, 8 tokens 43; 16384: 8 tokens 70, 2
-  // tokens 74)
+  // about 2048 blocks, fewer tokens in each of a shorter call (40 heads of 128;
+  // 4096 tokens, fp32: 2 tokens a block 30.7 us, 8 tokens 34.9; 16384, bf16: 8
+  // tokens 63.3, 2 tokens 69.4)
   a.toks = (int)std::max<int64_t>(1, std::min<int64_t>(8, n / 2048));
   a.sign = sign;
   if (q->in_dtype == HGA_BF16)
@@ -1247,15 +1247,19 @@ struct Q4Plan {
 };
 
 // tcgen05 takes 256 rows at the price of one and expands K and V once for them,
-// but a CTA of it costs about 20 us to start and end.  Times in us, dense, 32
-// heads on 4, d 128, sequences x context, mma.sync / tcgen05:
-//   rows       32         64         128        256
-//   1 x 16384  20 / 51    24 / 52    34 / 53    70 / 56
-//   8 x 8192   37 / 51    84 / 52    99 / 53   182 / 61
-//   32 x 4096  59 / 75    99 / 77   178 / 78   341 / 94
-//   8 x 1024   18 / 24    25 / 24    26 / 25    35 / 28
-// so: from 64 rows on, if the 16-row tiles of mma.sync have more tokens to go
-// over than this, all together.
+// but a CTA of it costs about 20 us to start and end.  Times in us of one call
+// with the cache flushed, dense, 32 heads on 4, d 128, sequences x context,
+// mma.sync / tcgen05:
+//   rows       64         128        256
+//   1 x 16384  32 / 58    40 / 58    77 / 62
+//   8 x 8192   91 / 58   107 / 60   188 / 66
+//   32 x 4096 107 / 82   184 / 82   344 / 92
+//   8 x 1024   32 / 30    32 / 30    42 / 34
+// (with 32 rows mma.sync was faster in the first three by 14 us or more.)
+// So: from 64 rows on, if the 16-row tiles of mma.sync have more tokens to go
+// over than this, all together.  Two of the table's calls have exactly as many:
+// 8 x 1024 with 256 rows loses 8 us by the rule, 1 x 16384 with 128 would lose
+// 18 if they went the other way.
 constexpr int64_t kQ4TcMinRows = 64, kQ4TcMinWork = 1 << 19;
 
 // rows, max_tok: most query rows and tokens of a unit; n_seq: sequences of a

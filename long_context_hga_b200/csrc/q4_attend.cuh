@@ -258,9 +258,11 @@ __device__ __forceinline__ void q4_fetch8(char* dst, const char* base, int64_t a
 
 // The batch's tokens dealt out to `slots` CTAs (more than sequences): every
 // sequence gets as many as its length needs at `per` steps each, at least one,
-// with `per` the least that makes them suffice: sum ceil(steps / per) <= n_seq +
-// total / per.  Only the device knows the lengths, and a split into as many
-// parts for every sequence leaves the longest ones' CTAs running last.
+// with a `per` that always suffices: sum ceil(steps / per) <= n_seq + total / per.
+// It is not the least one: with lengths between half and all of the longest it
+// is up to 1.1 times that for 8 sequences on 111 CTAs, 1.6 times for 32 on 55.  Only
+// the device knows the lengths, and a split into as many parts for every
+// sequence leaves the longest ones' CTAs running last.
 __device__ __forceinline__ int q4_seq_steps(const Q4AttendArgs& g, int z) {
   const int r = g.b.rows[z];
   if (r < 0 || r >= g.c.n_rows) return 0;
