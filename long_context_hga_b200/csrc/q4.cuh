@@ -263,8 +263,9 @@ __device__ __forceinline__ void q4_block_tokens(const Q4IoArgs& a, int64_t t0, i
 
 // One thread per 8 values of K and the same 8 of V, so that a warp's 16-byte
 // loads are contiguous; the two threads of a scale exchange their maxima.
-// Bound: HBM (reads 4 d, writes 9 d / 8 bytes per token and head) and nearly as
-// much the issue slots of the encoding: 32768 tokens, 8 heads of 128, bf16: 43 us.
+// It reads 4 d and writes 9 d / 8 bytes per token and head.  Bound: a block's one
+// chain (places of its tokens, a barrier, loads, encoding) beside the issue slots
+// (65 % taken, ALU 57 %, HBM 40 %): 32768 tokens, 8 heads of 128, bf16: 43 us.
 template <typename T>
 __global__ void __launch_bounds__(kQ4Threads) q4_append_kernel(const Q4IoArgs a) {
   __shared__ Q4BlockTokens tok;
@@ -341,8 +342,9 @@ __device__ __forceinline__ void q4_decode8(uint32_t codes, int scale, T* out) {
 }
 
 // The batch's tokens back as the values their codes stand for, in TK and TV.
-// One thread per 8 values of K and of V: contiguous 16-byte stores.  Bound: HBM
-// and the latency of its small loads: 32768 tokens, 8 heads of 128: 36 us.
+// One thread per 8 values of K and of V: contiguous 16-byte stores.  Bound: the
+// latency of the look-up and the small loads (the largest stall; issue slots 55 %,
+// HBM 39 %): 32768 tokens, 8 heads of 128: 36 us.
 template <typename TK, typename TV>
 __global__ void __launch_bounds__(kQ4Threads) q4_read_kernel(const Q4IoArgs a) {
   __shared__ Q4BlockTokens tok;

@@ -16,9 +16,10 @@
 // of two of its row (bf16: exact up to 2^-25 of the row's maximum; fp32: as a
 // sum of two fp16 values, like P, 22 bits).  Sums, maxima and O are fp32.
 //
-// Bound: the issue slots of the conversions and products, which hold HBM (4.5
-// bits a value) at half its rate: 8 sequences of 32K to 64K tokens, 32 heads on
-// 4, d 128, with the append and the join: 66 us for 237 MB.  Each warp runs
+// Bound: no unit is full (issue slots 57 %, ALU 52 %, HBM 49 %): a warp's step is
+// one chain of loads, conversions, products and softmax, and the registers allow
+// 12 warps an SM.  8 sequences of 32K to 64K tokens, 32 heads on 4, d 128, with
+// the append and the join: 66 us for 237 MB.  Each warp runs
 // alone: it fetches 64 tokens (8 records) at a time into its own ring by bulk copies and
 // never waits for another warp until the end, where the CTA's warps join their
 // (max, sum, O), and a second kernel joins the splits of a long context, in a
